@@ -94,6 +94,10 @@ _SIGS = {
     "nc_attention_bwd_ex": (_I, [_P, ctypes.c_int64, _P, _P, _P, _P, _P, ctypes.c_size_t, _P, _I, _I, _I, _I,
                                  _I, _I, _P]),
     "nc_set_attention_ctas": (_I, [_I]),
+    "nc_add_rmsnorm_fp8": (_I, [_P, _P, _P, _P, _P, ctypes.c_int64, _P, _I, _I, _I, _P]),
+    "nc_quant_fp8": (_I, [_P, ctypes.c_int64, _P, ctypes.c_int64, _P, ctypes.c_int64, _I, _I, _I, _I, _P]),
+    "nc_gemm_fp8": (_I, [_P, ctypes.c_int64, _P, ctypes.c_int64, _P, ctypes.c_int64, _P, ctypes.c_int64, _P,
+                         ctypes.c_int64, _P, ctypes.c_int64, _I, _I, _I, _I, _P]),
     "nc_rmsnorm": (_I, [_P, _P, _P, _I, _I, _I, _P]),
     "nc_rmsnorm_bwd": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _P]),
     "nc_rope_qknorm": (_I, [_P, _P, ctypes.c_int64, _P, _P, _I, _I, _P]),
@@ -106,6 +110,7 @@ NC_EPI_ADD = 2
 NC_EPI_RELU2 = 3
 NC_EPI_DRELU2 = 4
 NC_EPI_SOFTCAP = 5
+NC_EPI_RELU2_FP8 = 7  # nc_gemm_fp8 only
 
 
 def load_library(path: str = LIB_PATH):
@@ -324,6 +329,21 @@ def nc_rope_qknorm(handle, qkv, ld, rq, rk, B, T, stream) -> int:
 
 def nc_rope_qknorm_bwd(handle, dqkv, qkv, ld, rq, rk, B, T, stream) -> int:
     return load_library().nc_rope_qknorm_bwd(handle, dqkv, qkv, ld, rq, rk, B, T, stream)
+
+
+def nc_add_rmsnorm_fp8(x, res, x_out, q, s, lds, r, M, C, dtype, stream) -> int:
+    """x_out = x + res, then RMSNorm, its output in e4m3 with a scale per 1 x 128 block (res, r may be None)."""
+    return load_library().nc_add_rmsnorm_fp8(x, res, x_out, q, s, lds, r, M, C, dtype, stream)
+
+
+def nc_quant_fp8(x, ldx, q, ldq, s, lds, rows, cols, block_rows, dtype, stream) -> int:
+    """A matrix in e4m3 with a scale per 1 x 128 (block_rows 1) or 128 x 128 (block_rows 128) block."""
+    return load_library().nc_quant_fp8(x, ldx, q, ldq, s, lds, rows, cols, block_rows, dtype, stream)
+
+
+def nc_gemm_fp8(A, lda, sa, lsa, B, ldb, sb, lsb, D, ldd, sd, lsd, M, N, K, epilogue, stream) -> int:
+    """D = epilogue(A B^T) of e4m3 operands with block scales (sd: the scales of an 8-bit D, else None)."""
+    return load_library().nc_gemm_fp8(A, lda, sa, lsa, B, ldb, sb, lsb, D, ldd, sd, lsd, M, N, K, epilogue, stream)
 
 
 def nc_ops_status(stream, timeout_ms: int) -> int:

@@ -18,6 +18,10 @@ namespace nc {
 // Rows up to C = 32 lanes * 16 * 8 = 4096 are supported.
 constexpr int kMaxVecPerLane = 16;
 
+inline unsigned rows_grid(size_t rows, int rows_per_block) {
+  return (unsigned)((rows + rows_per_block - 1) / rows_per_block);
+}
+
 #define NC_DISPATCH_NV(C, KERNEL_CALL)                 \
   do {                                                 \
     const int nv_ = ((C) / 8 + 31) / 32;               \

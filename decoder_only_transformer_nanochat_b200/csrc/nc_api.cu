@@ -25,6 +25,7 @@
 #include "attn_simt.cuh"
 #include "ce.cuh"
 #include "elementwise.cuh"
+#include "gemm_fp8.cuh"
 #include "gemm_simt.cuh"
 #include "gemm_tc.cuh"
 #include "optim.cuh"
@@ -278,10 +279,6 @@ inline GemmProblem gp(int M, int N, int K, const void *A, int64_t lda, int a_mn,
   p.M = M; p.N = N; p.K = K; p.A = A; p.lda = lda; p.a_mn = a_mn; p.B = B; p.ldb = ldb;
   p.b_mn = b_mn; p.D = D; p.ldd = ldd; p.epi = epi;
   return p;
-}
-
-inline unsigned rows_grid(size_t rows, int rows_per_block) {
-  return (unsigned)((rows + rows_per_block - 1) / rows_per_block);
 }
 
 #define NC_TRY(x)              \
@@ -576,6 +573,7 @@ struct SymbolAddrs {
   unsigned long long ctx_id;
   int *ops_status;
   float *rowdot;
+  int fp8_sms;  // SM count once the 8-bit GEMM's kernels are set up here, else 0
 };
 typedef CUresult (*CtxGetCurrentFn)(CUcontext *);
 typedef CUresult (*CtxGetIdFn)(CUcontext, unsigned long long *);
@@ -626,6 +624,7 @@ int symbol_addrs(SymbolAddrs *out) {
     return NC_ECUDA;
   e.ops_status = static_cast<int *>(p1);
   e.rowdot = static_cast<float *>(p2);
+  e.fp8_sms = 0;
   g_sym_cache.push_back(e);
   *out = e;
   return NC_OK;
@@ -640,6 +639,26 @@ int op_setup(int *num_sms, int **status) {
   if (tc_init() != cudaSuccess || fatc::init() != cudaSuccess || ce_init() != cudaSuccess) return NC_ECUDA;
   SymbolAddrs a;
   if (symbol_addrs(&a) != NC_OK) return NC_ECUDA;
+  *status = a.ops_status;
+  return NC_OK;
+}
+
+// The same for the 8-bit GEMM, done once per context: at one decoded token the
+// set-up calls would take as long as the kernel.
+int fp8_setup(int *num_sms, int **status) {
+  SymbolAddrs a;
+  if (symbol_addrs(&a) != NC_OK) return NC_ECUDA;
+  if (!a.fp8_sms) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&a.fp8_sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+        tc8::init() != cudaSuccess)
+      return NC_ECUDA;
+    std::lock_guard<std::mutex> lock(g_sym_mutex);
+    for (SymbolAddrs &e : g_sym_cache)
+      if (e.ctx_id == a.ctx_id) e.fp8_sms = a.fp8_sms;
+  }
+  *num_sms = a.fp8_sms;
   *status = a.ops_status;
   return NC_OK;
 }
@@ -1359,6 +1378,66 @@ int nc_rope_qknorm_bwd(const nc_model *m, void *dqkv, const void *qkv, int64_t l
     rope_qknorm_bwd_kernel<float><<<rows_grid((size_t)M, 8), 256, 0, st>>>(
         (float *)dqkv, (const float *)qkv, (int)ld, rq, rk, m->rope_cos, m->rope_sin, M, T, m->H);
   return cudaGetLastError() == cudaSuccess ? NC_OK : NC_ECUDA;
+}
+
+int nc_add_rmsnorm_fp8(const void *x, const void *res, void *x_out, void *q, float *s, int64_t lds, float *r, int M,
+                       int C, int dtype, void *stream) {
+  if (!x || !x_out || !q || !s) return NC_EINVAL;
+  if (M < 1 || C < 16 || C % 16 || C > 32 * kMaxVecPerLane * 8 || lds < M) return NC_ESHAPE;
+  if (dtype != NC_F32 && dtype != NC_BF16) return NC_EUNSUPPORTED;
+  if ((((uintptr_t)x | (uintptr_t)res | (uintptr_t)x_out | (uintptr_t)q) & 15) || (((uintptr_t)s | (uintptr_t)r) & 3))
+    return NC_EALIGN;
+  const cudaError_t e =
+      dtype == NC_BF16 ? fp8::launch_add_rmsnorm<bf16>((const bf16 *)x, (const bf16 *)res, (bf16 *)x_out, (uint8_t *)q,
+                                                       s, lds, r, M, C, (cudaStream_t)stream)
+                       : fp8::launch_add_rmsnorm<float>((const float *)x, (const float *)res, (float *)x_out,
+                                                        (uint8_t *)q, s, lds, r, M, C, (cudaStream_t)stream);
+  return e == cudaSuccess ? NC_OK : NC_ECUDA;
+}
+
+int nc_quant_fp8(const void *x, int64_t ldx, void *q, int64_t ldq, float *s, int64_t lds, int rows, int cols,
+                 int block_rows, int dtype, void *stream) {
+  if (!x || !q || !s) return NC_EINVAL;
+  if (block_rows != 1 && block_rows != 128) return NC_EINVAL;
+  const int kbs = (cols + 127) / 128;
+  if (rows < 1 || cols < 16 || cols % 16 || cols > (1 << 30) || ldx < cols || ldq < cols ||
+      lds < (block_rows == 1 ? rows : kbs))
+    return NC_ESHAPE;
+  if (dtype != NC_F32 && dtype != NC_BF16) return NC_EUNSUPPORTED;
+  if ((((uintptr_t)x | (uintptr_t)q) & 15) || ((uintptr_t)s & 3) || ldx % (dtype == NC_BF16 ? 8 : 4) || ldq % 16)
+    return NC_EALIGN;
+  const cudaError_t e =
+      dtype == NC_BF16 ? fp8::launch_quant<bf16>((const bf16 *)x, ldx, (uint8_t *)q, ldq, s, lds, rows, cols, block_rows,
+                                                 (cudaStream_t)stream)
+                       : fp8::launch_quant<float>((const float *)x, ldx, (uint8_t *)q, ldq, s, lds, rows, cols,
+                                                  block_rows, (cudaStream_t)stream);
+  return e == cudaSuccess ? NC_OK : NC_ECUDA;
+}
+
+int nc_gemm_fp8(const void *A, int64_t lda, const float *sa, int64_t lsa, const void *B, int64_t ldb, const float *sb,
+                int64_t lsb, void *D, int64_t ldd, float *sd, int64_t lsd, int M, int N, int K, int epilogue,
+                void *stream) {
+  if (!A || !sa || !B || !sb || !D) return NC_EINVAL;
+  const bool f8 = epilogue == NC_EPI_RELU2_FP8, f32 = epilogue == NC_EPI_STORE_F32;
+  if (!f8 && !f32 && epilogue != NC_EPI_STORE && epilogue != NC_EPI_ADD && epilogue != NC_EPI_RELU2 &&
+      epilogue != NC_EPI_SOFTCAP)
+    return NC_EINVAL;
+  if (f8 && !sd) return NC_EINVAL;
+  const int most = 1 << 30;
+  if (M < 1 || N < 1 || K < 1 || M > most || N > most || K > most) return NC_ESHAPE;
+  if (lda < K || ldb < K || ldd < N || lsa < M || lsb < (K + 127) / 128 || (f8 && lsd < M)) return NC_ESHAPE;
+  if ((((uintptr_t)A | (uintptr_t)B | (uintptr_t)D) & 15) || (((uintptr_t)sa | (uintptr_t)sb) & 3) ||
+      (f8 && ((uintptr_t)sd & 3)) || lda % 16 || ldb % 16 || ldd % (f8 ? 16 : f32 ? 4 : 8))
+    return NC_EALIGN;
+  int num_sms = 0, *status = nullptr;
+  if (fp8_setup(&num_sms, &status) != NC_OK) return NC_ECUDA;
+  GemmFp8Problem g;
+  g.M = M; g.N = N; g.K = K;
+  g.A = A; g.lda = lda; g.sa = sa; g.lsa = lsa;
+  g.B = B; g.ldb = ldb; g.sb = sb; g.lsb = lsb;
+  g.D = D; g.ldd = ldd; g.sd = sd; g.lsd = lsd;
+  g.epi = epilogue;
+  return launch_gemm_fp8(g, num_sms, status, (cudaStream_t)stream) == cudaSuccess ? NC_OK : NC_ECUDA;
 }
 
 int nc_set_attention_ctas(int ctas) {

@@ -193,6 +193,66 @@ int nc_rope_qknorm(const nc_model *m, void *qkv, int64_t ld, float *rq, float *r
 int nc_rope_qknorm_bwd(const nc_model *m, void *dqkv, const void *qkv, int64_t ld, const float *rq,
                        const float *rk, int B, int T, void *stream);
 
+/* 8-bit operands of the serving path ("nanochat-train", "Precision / dtype":
+ * FP8 beside bf16).  Values are held in e4m3 (largest value 448) with one fp32
+ * scale per block of 128: a block whose largest magnitude is a is held as
+ *   q = round_to_nearest_even_e4m3(448 v / a),  s = a / 448,  v ~ q s
+ * and an all-zero block as q = 0, s = 0.  bf16 inputs get the code of the
+ * exact quotient, fp32 inputs that of RN(RN(448 v) / a).  A NaN gets the e4m3
+ * NaN; a block with an infinity gets an infinite scale and NaN in its place,
+ * so neither is lost in the product.
+ * Activations (rows of the product) are cut into 1 x 128 blocks, their scales
+ * stored k-block-major: s[kb * lds + row], lds >= rows; weights into
+ * 128 x 128 blocks, s[nb * lds + kb], lds >= ceil(cols / 128).  A last block
+ * shorter than 128 has a scale of its own.  These calls run forward only:
+ * the 8-bit copies serve, the weights that train stay in the model dtype.
+ *
+ * The residual's addition, RMSNorm and the 8-bit operand of the projection
+ * that follows, in one pass:
+ *   x_out[m,c] = x[m,c] + res[m,c]   (rounded to dtype; res NULL: x itself)
+ *   r[m] = 1 / sqrt(mean_c x_out[m,c]^2 + 2^-23)
+ *   q, s = 1 x 128 blocks of x_out[m,c] r[m]
+ * x, res, x_out: [M, C] rows in dtype, x_out may equal x or res; q: [M, C]
+ * e4m3; r: [M] fp32 or NULL.  The codes come from x_out (the norm scales a
+ * row as a whole), s = r max|x_out| / 448.  A row that holds a NaN or an
+ * infinity gets scales that are NaN in the blocks holding it at least.
+ * 16 <= C <= 4096 with C % 16 == 0, lds >= M (else NC_ESHAPE); x, res, x_out,
+ * q 16-byte aligned, s and r 4-byte aligned (else NC_EALIGN). */
+int nc_add_rmsnorm_fp8(const void *x, const void *res, void *x_out, void *q, float *s, int64_t lds, float *r,
+                       int M, int C, int dtype, void *stream);
+
+/* A matrix x [rows, cols] (dtype, row stride ldx elements) in 8 bits: q e4m3
+ * with row stride ldq, s as above for block_rows 1 (activations: attention
+ * outputs before their projection) or 128 (weights).  cols >= 16 with
+ * cols % 16 == 0 (else NC_ESHAPE); x and q 16-byte aligned with 16-byte row
+ * strides (else NC_EALIGN); other block_rows: NC_EINVAL. */
+int nc_quant_fp8(const void *x, int64_t ldx, void *q, int64_t ldq, float *s, int64_t lds, int rows, int cols,
+                 int block_rows, int dtype, void *stream);
+
+/* relu(acc)^2 left in 8 bits by 1 x 128 blocks, the A operand of the next
+ * product (nc_gemm_fp8 only) */
+#define NC_EPI_RELU2_FP8 7
+
+/* Product of 8-bit operands:
+ *   acc[m,n] = sum_kb sa[kb*lsa + m] sb[(n/128)*lsb + kb] sum_{k in block kb} A[m*lda + k] B[n*ldb + k]
+ *   D[m*ldd + n] = epilogue(acc)
+ * A: activations [M, K] with 1 x 128 scales, B: weights [N, K] with 128 x 128
+ * scales (y = x W^T).  Each block of K is summed on the tensor cores and the
+ * scaled blocks in fp32, in an order that depends on the shape alone: the
+ * same call gives the same bits.
+ * epilogue: NC_EPI_STORE, _ADD (D += acc), _RELU2 or _SOFTCAP with D bf16,
+ * NC_EPI_STORE_F32 with D fp32, or NC_EPI_RELU2_FP8 with D e4m3 and its scales
+ * in sd[(n/128)*lsd + m]; sd and lsd are not looked at otherwise.  Others:
+ * NC_EINVAL.
+ * 1 <= M, N, K <= 2^30, lda, ldb >= K, ldd >= N, lsa (and lsd) >= M,
+ * lsb >= ceil(K / 128), else NC_ESHAPE; A, B, D 16-byte aligned with 16-byte
+ * row strides, the scales 4-byte aligned, else NC_EALIGN.  D and sd must not
+ * overlap the operands.  A wait that ran out of time is reported through
+ * nc_ops_status. */
+int nc_gemm_fp8(const void *A, int64_t lda, const float *sa, int64_t lsa, const void *B, int64_t ldb,
+                const float *sb, int64_t lsb, void *D, int64_t ldd, float *sd, int64_t lsd, int M, int N, int K,
+                int epilogue, void *stream);
+
 /* Cap on the CTAs of the persistent attention kernels (the forward and the
  * dQ kernel of the backward, in nc_fwd_bwd and the op-level calls): 0 (the
  * default) = one CTA per SM; n > 0 = at most n CTAs, each then taking more
