@@ -63,6 +63,13 @@ __device__ __forceinline__ void tmem_ld16_nw(uint32_t taddr, uint32_t (&r)[16]) 
       : "r"(taddr));
 }
 
+// the wait for those loads; the registers pass through it, so nothing that uses them can move above
+__device__ __forceinline__ void tmem_wait16(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
+}
+
 // 15 tanh(z / 15) from one exponential: t = (1 - E) / (1 + E), E = exp(-2 |z| / 15)
 __device__ __forceinline__ float softcap8(float z) {
   const float e = __expf(-2.f / kSoftcap * fabsf(z));
@@ -283,7 +290,7 @@ __global__ void __launch_bounds__(RowsCfg<TN>::kThreads, 2)
       for (int c = 0; c < COLS; c += 16) {
         uint32_t v[16];
         tmem_ld16_nw(t + c, v);
-        tmem_wait_ld();
+        tmem_wait16(v);
 #pragma unroll
         for (int j = 0; j < 16; j += 4) {
           const float4 f = *reinterpret_cast<const float4 *>(sw + c + j);
@@ -323,6 +330,391 @@ __global__ void __launch_bounds__(RowsCfg<TN>::kThreads, 2)
   }
 }
 
+// ===========================================================================
+// Many rows: a pair of CTAs (cta_group::2) on neighbouring SMs takes a
+// 256 x 256 tile, as the bf16 GEMM's pair kernel does (gemm_tc.cuh): CTA r
+// holds tile rows [128 r, 128 r + 128) of A and of the accumulator and loads
+// half of B; the leader (r = 0) issues every MMA.  Persistent, one CTA per SM.
+//
+// TMEM holds two 256-column accumulators, one K block each: while the tensor
+// cores fill one, the eight epilogue warps of each CTA scale and add the other
+// into fp32 sums in registers (thread = one row x 128 columns: one weight
+// block, so one scale per thread and K block).  Per K block and SM the MMAs
+// take 512 cycles at the full rate, the TMEM reads 256 and the packed
+// multiply-adds 128 issue slots per scheduler: the tensor pipe stays the bound.
+// A thread's 128 columns are also one 1 x 128 output block, so the 8-bit
+// epilogue finds its maximum without leaving the thread.
+//
+// Each epilogue warp stages its 32 rows x 128 columns alone, in two boxes of
+// 32 rows x 128 bytes (128-byte swizzle) that leave by TMA; an epilogue that
+// adds to D has them loaded while the K loop runs.
+constexpr int PSTAGES = 5;
+constexpr int PSTAGE_BYTES = 2 * 128 * BK;  // A and B rows of one CTA: 32 KB
+constexpr int PEPI_WARPS = 8;
+// Three warpgroups: warp 0 TMA, warp 1 MMA (warps 2, 3 idle), warps 4..11 the
+// epilogue, which holds 128 sums a thread.  The first gives registers to the
+// others: 128 x 56 + 256 x 224 = 64,512, all of the 384 x 168 of the launch
+// (init() checks that count), so every increase can be met.
+constexpr int PTHREADS = 128 + 32 * PEPI_WARPS;
+constexpr int PREGS = 168, PREGS_LOW = 56, PREGS_HIGH = 224;
+static_assert(128 * PREGS_LOW + 32 * PEPI_WARPS * PREGS_HIGH <= PTHREADS * PREGS, "register split within the launch");
+constexpr int PBOX = 32 * 128;
+constexpr int PSMEM = PSTAGES * PSTAGE_BYTES + PEPI_WARPS * 2 * PBOX + 256 + 1024;
+static_assert(PSMEM <= 232448, "shared memory per CTA");
+
+// A TMA store writes whole 16-byte units of a row (measured: one byte per
+// element, N % 16 == 8, wrote eight bytes past N), so the map of D ends at the
+// last whole unit, column n_tma, and the threads take the rest of their row.
+struct PairParams {
+  int M, N, kblocks;
+  int n_m, n_n, units, n_tma;
+  void *D;
+  int64_t ldd;
+  const float *sa, *sb;
+  int64_t lsa, lsb;
+  float *sd;
+  int64_t lsd;
+  int epi;
+  int *status;
+};
+
+// The columns [n_tma, N) of row m that lie in [n, n + width): from or to the
+// warp's staged boxes (row at `my`, column n at byte 0), es bytes each.
+template <bool kLoad, typename E>
+__device__ __forceinline__ void pair_tail(const PairParams &p, uint8_t *my, int lane, int m, int n, int width) {
+  if (m >= p.M) return;
+  for (int c = max(p.n_tma, n); c < min(p.N, n + width); ++c) {
+    const int b = (c - n) * (int)sizeof(E);
+    E *e = reinterpret_cast<E *>(my + (b >> 7) * PBOX + ((((b >> 4) & 7) ^ (lane & 7)) << 4) + (b & 15));
+    E *d = reinterpret_cast<E *>(p.D) + (int64_t)m * p.ldd + c;
+    if (kLoad) *e = *d;
+    else *d = *e;
+  }
+}
+
+__device__ __forceinline__ void mma8_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Tiles in flight at once share operand panels in L2: with few N tiles those
+// of an M block are consecutive, with many 16 M blocks share each B panel.
+__device__ __forceinline__ void pair_tile(const PairParams &p, int u, int &m_blk, int &n_blk) {
+  if (p.n_n <= 16) {
+    m_blk = u / p.n_n;
+    n_blk = u % p.n_n;
+    return;
+  }
+  const int G = 16, per = G * p.n_n, first = u / per * G, size = min(p.n_m - first, G), r = u % per;
+  m_blk = first + r % size;
+  n_blk = r / size;
+}
+
+__global__ void __launch_bounds__(PTHREADS, 1)
+    gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                         const __grid_constant__ CUtensorMap map_d, const PairParams p) {
+  constexpr int S = PSTAGES;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t *staging = smem + S * PSTAGE_BYTES;
+  uint64_t *bars = reinterpret_cast<uint64_t *>(staging + PEPI_WARPS * 2 * PBOX);
+  // bars: full[S], empty[S], tfull[2], tempty[2], drain, aux[PEPI_WARPS]
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * S + 5 + PEPI_WARPS);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+  static_assert((2 * S + 5 + PEPI_WARPS) * 8 + 8 <= 256, "barriers, TMEM slot and abort flag fit their 256 bytes");
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const bool leader = rank == 0;
+  const int cluster = blockIdx.x >> 1, n_clusters = gridDim.x >> 1;
+  auto full_bar = [&](int s) { return smem_u32(bars + s); };
+  auto empty_bar = [&](int s) { return smem_u32(bars + S + s); };
+  auto tfull_bar = [&](int a) { return smem_u32(bars + 2 * S + a); };
+  auto tempty_bar = [&](int a) { return smem_u32(bars + 2 * S + 2 + a); };
+  const uint32_t drain_bar = smem_u32(bars + 2 * S + 4);
+  auto aux_bar = [&](int w) { return smem_u32(bars + 2 * S + 5 + w); };
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(tfull_bar(a), 1);
+      mbar_init(tempty_bar(a), 2 * PEPI_WARPS);  // both CTAs' epilogue warps
+    }
+    mbar_init(drain_bar, 1);
+    for (int w = 0; w < PEPI_WARPS; ++w) mbar_init(aux_bar(w), 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                 "r"(TMEM_COLS)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();  // both CTAs' barriers exist before any cross-CTA signal
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+
+  if (warp < 4) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(PREGS_LOW));
+  if (warp == 0) {
+    if (lane == 0) {
+      // ---------------- TMA producer ----------------
+      int stage = 0, issued = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int u = cluster; u < p.units && ok; u += n_clusters) {
+        int m_blk, n_blk;
+        pair_tile(p, u, m_blk, n_blk);
+        const int m_row = m_blk * 256 + (int)rank * 128, n_row = n_blk * 256 + (int)rank * 128;
+        for (int kb = 0; kb < p.kblocks; ++kb) {
+          if (!mbar_wait<true>(empty_bar(stage), phase ^ 1, abort_flag, p.status)) { ok = false; break; }
+          const uint32_t sa = smem_u32(smem + stage * PSTAGE_BYTES);
+          if (leader) mbar_expect_tx(full_bar(stage), 2 * PSTAGE_BYTES);
+          const uint32_t fb = cluster_addr(full_bar(stage), 0);
+          tma_load_2d_pair(sa, &map_a, kb * BK, m_row, fb);
+          tma_load_2d_pair(sa + 128 * BK, &map_b, kb * BK, n_row, fb);
+          issued = min(issued + 1, S);
+          if (++stage == S) { stage = 0; phase ^= 1; }
+        }
+      }
+      // both CTAs' copies count on the leader's barriers: it sees them landed
+      // (bounded) before the final cluster barrier lets either CTA exit
+      if (leader)
+        for (int i = 0; i < issued; ++i) {
+          if (--stage < 0) { stage = S - 1; phase ^= 1; }
+          const uint64_t t0 = globaltimer();
+          while (!mbar_try(full_bar(stage), phase) && globaltimer() - t0 < kWaitNs) {}
+        }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && leader) {
+      // ---------------- MMA issuer ----------------
+      const uint32_t idesc = idesc8(256, 256);
+      int stage = 0, acc = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      bool ok = true;
+      for (int u = cluster; u < p.units && ok; u += n_clusters) {
+        for (int kb = 0; kb < p.kblocks; ++kb) {
+          if (!mbar_wait<true>(tempty_bar(acc), acc_phase ^ 1, abort_flag, p.status) ||
+              !mbar_wait<true>(full_bar(stage), phase, abort_flag, p.status)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sa = smem_u32(smem + stage * PSTAGE_BYTES), sb = sa + 128 * BK;
+#pragma unroll
+          for (int kk = 0; kk < BK / 32; ++kk)
+            mma8_pair(tmem_base + acc * 256, smem_desc(sa + kk * 32, 16, 1024), smem_desc(sb + kk * 32, 16, 1024), idesc,
+                      kk > 0);
+          tc_commit_pair(empty_bar(stage), 0x3);
+          tc_commit_pair(tfull_bar(acc), 0x3);
+          if (++stage == S) { stage = 0; phase ^= 1; }
+          if (++acc == 2) { acc = 0; acc_phase ^= 1; }
+        }
+      }
+      tc_commit_pair(drain_bar, 0x1);
+      const uint64_t t0 = globaltimer();
+      while (!mbar_try(drain_bar, 0) && globaltimer() - t0 < kWaitNs) {}
+    }
+  }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(PREGS_HIGH));
+    // ---------------- epilogue warps 4..11 (both CTAs) ----------------
+    const int quarter = warp & 3;
+    const int cg = (warp - 4) >> 2;  // columns [128 cg, 128 cg + 128) of the tile
+    const uint32_t t_row = tmem_base + ((uint32_t)(quarter * 32) << 16) + cg * 128;
+    uint8_t *const box = staging + (warp - 4) * 2 * PBOX;
+    uint8_t *const my = box + lane * 128;  // 16-byte unit u of this row's 128 bytes sits at u ^ (row % 8)
+    const uint32_t aux = aux_bar(warp - 4);
+    uint32_t aux_phase = 0;
+    bool aux_inflight = false;
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    bool ok = true;
+    // this thread's scale of K block kb in unit u
+    auto scale_of = [&](int u, int kb) {
+      int m_blk, n_blk;
+      pair_tile(p, u, m_blk, n_blk);
+      const int m = m_blk * 256 + (int)rank * 128 + quarter * 32 + lane, nb = n_blk * 2 + cg;
+      if (m >= p.M || nb * 128 >= p.N) return 0.f;
+      return p.sa[(int64_t)kb * p.lsa + m] * p.sb[(int64_t)nb * p.lsb + kb];
+    };
+    float next = cluster < p.units ? scale_of(cluster, 0) : 0.f;
+    for (int u = cluster; u < p.units; u += n_clusters) {
+      int m_blk, n_blk;
+      pair_tile(p, u, m_blk, n_blk);
+      const int mw = m_blk * 256 + (int)rank * 128 + quarter * 32;  // this warp's first row
+      const int n0 = n_blk * 256 + cg * 128;
+      const bool mine = mw < p.M && n0 < p.N;
+      const bool by_tma = n0 < p.n_tma, two = n0 + 64 < p.n_tma;
+      if (p.epi == EPI_ADD && mine && by_tma && lane == 0) {
+        bulk_wait_read0();  // the previous tile's stores have read the boxes
+        mbar_expect_tx(aux, two ? 2 * PBOX : PBOX);
+        tma_load_2d(smem_u32(box), &map_d, n0, mw, aux);
+        if (two) tma_load_2d(smem_u32(box) + PBOX, &map_d, n0 + 64, mw, aux);
+        aux_inflight = true;
+      }
+      uint64_t sum[64];
+#pragma unroll
+      for (int i = 0; i < 64; ++i) sum[i] = 0;
+      for (int kb = 0; kb < p.kblocks; ++kb) {
+        const uint64_t f = f2(next, next);
+        // the next block's scale, or the next tile's first
+        if (kb + 1 < p.kblocks) next = scale_of(u, kb + 1);
+        else if (u + n_clusters < p.units) next = scale_of(u + n_clusters, 0);
+        ok = __all_sync(0xffffffffu, mbar_wait<true>(tfull_bar(acc), acc_phase, abort_flag, p.status));
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t t = t_row + acc * 256;
+        uint32_t v[2][16];
+        tmem_ld16_nw(t, v[0]);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          tmem_wait16(v[c & 1]);
+          if (c < 7) tmem_ld16_nw(t + 16 * (c + 1), v[(c + 1) & 1]);
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            sum[8 * c + j] = fma2(f2(__uint_as_float(v[c & 1][2 * j]), __uint_as_float(v[c & 1][2 * j + 1])), f,
+                                  sum[8 * c + j]);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (leader) mbar_arrive(tempty_bar(acc));
+          else mbar_arrive_remote(tempty_bar(acc), 0);
+        }
+        if (++acc == 2) { acc = 0; acc_phase ^= 1; }
+      }
+      if (!ok) break;
+      if (!mine) continue;
+      if (p.epi == EPI_ADD && by_tma) {
+        ok = __all_sync(0xffffffffu, mbar_wait<true>(aux, aux_phase, abort_flag, p.status));
+        if (!ok) break;
+        aux_phase ^= 1;
+        aux_inflight = false;
+      } else {
+        if (lane == 0) bulk_wait_read0();
+        __syncwarp();
+      }
+      if (p.epi == EPI_STORE_F32) {
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          if (b == 2) {
+            if (lane == 0) bulk_wait_read0();
+            __syncwarp();
+          }
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            float o[4];
+            f2split(sum[16 * b + 2 * q], o[0], o[1]);
+            f2split(sum[16 * b + 2 * q + 1], o[2], o[3]);
+            *reinterpret_cast<float4 *>(my + (b & 1) * PBOX + ((q ^ (lane & 7)) << 4)) = make_float4(o[0], o[1], o[2], o[3]);
+          }
+          if (b & 1) {
+            const int n = n0 + (b - 1) * 32;
+            pair_tail<false, float>(p, my, lane, mw + lane, n, 64);
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) {
+              if (n < p.n_tma) tma_store_2d(&map_d, smem_u32(box), n, mw);
+              if (n + 32 < p.n_tma) tma_store_2d(&map_d, smem_u32(box) + PBOX, n + 32, mw);
+              bulk_commit();
+            }
+          }
+        }
+        continue;
+      }
+      if (p.epi == EPI_RELU2_FP8) {
+        float a = 0.f;
+#pragma unroll
+        for (int i = 0; i < 64; ++i) {
+          float lo, hi;
+          f2split(sum[i], lo, hi);
+          lo = lo < 0.f ? 0.f : lo;
+          hi = hi < 0.f ? 0.f : hi;
+          sum[i] = mul2(f2(lo, hi), f2(lo, hi));
+          f2split(sum[i], lo, hi);
+          a = fmaxf(a, fmaxf(lo, hi));
+        }
+        const fp8::Quant z(a);
+        const uint64_t f = f2(z.inv, z.inv), pre = f2(z.pre, z.pre);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          uint32_t w[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float o[4];
+            f2split(mul2(mul2(sum[8 * q + 2 * j], pre), f), o[0], o[1]);
+            f2split(mul2(mul2(sum[8 * q + 2 * j + 1], pre), f), o[2], o[3]);
+            w[j] = fp8::cvt2(o[0], o[1]) | (fp8::cvt2(o[2], o[3]) << 16);
+          }
+          *reinterpret_cast<uint4 *>(my + ((q ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        pair_tail<false, uint8_t>(p, my, lane, mw + lane, n0, 128);
+        if (mw + lane < p.M) p.sd[(int64_t)(n0 >> 7) * p.lsd + mw + lane] = __fdiv_rn(a, fp8::kMax);
+      } else {
+        if (p.epi == EPI_ADD) pair_tail<true, bf16>(p, my, lane, mw + lane, n0, 128);
+#pragma unroll
+        for (int q = 0; q < 16; ++q) {
+          bf16 *d = reinterpret_cast<bf16 *>(my + (q >> 3) * PBOX + (((q & 7) ^ (lane & 7)) << 4));
+          float o[8];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) f2split(sum[4 * q + j], o[2 * j], o[2 * j + 1]);
+          if (p.epi == EPI_ADD) {
+            float old[8];
+            Vec8<bf16>::load(d, old);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) o[j] += old[j];
+          } else if (p.epi == EPI_RELU2) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const float t = o[j] < 0.f ? 0.f : o[j];
+              o[j] = t * t;
+            }
+          } else if (p.epi == EPI_SOFTCAP) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) o[j] = softcap8(o[j]);
+          }
+          Vec8<bf16>::store(d, o);
+        }
+        pair_tail<false, bf16>(p, my, lane, mw + lane, n0, 128);
+      }
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) {
+        if (by_tma) tma_store_2d(&map_d, smem_u32(box), n0, mw);
+        if (p.epi != EPI_RELU2_FP8 && two) tma_store_2d(&map_d, smem_u32(box) + PBOX, n0 + 64, mw);
+        bulk_commit();
+      }
+    }
+    if (lane == 0) {
+      bulk_wait0();
+      // only after an abort: a load of D that was never taken lands first (bounded)
+      const uint64_t t0 = globaltimer();
+      while (aux_inflight && !mbar_try(aux, aux_phase) && globaltimer() - t0 < kWaitNs) {}
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();  // no CTA leaves while its peer can still signal or read it
+  tc_fence_after();
+  if (warp == 1) {
+    __syncwarp();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(TMEM_COLS)
+                 : "memory");
+  }
+}
+
 // ------------------------------- host side -------------------------------
 
 // 2D map over row-major bytes [rows, cols] with row stride ld, 128-byte swizzle
@@ -352,6 +744,48 @@ inline cudaError_t launch_rows(const GemmFp8Problem &g, int *status, cudaStream_
   return cudaGetLastError();
 }
 
+inline cudaError_t launch_pair(const GemmFp8Problem &g, int num_sms, int *status, cudaStream_t st) {
+  CUtensorMap ma, mb, md;
+  bool ok = make_map8(&ma, g.A, g.M, g.K, g.lda, 128) && make_map8(&mb, g.B, g.N, g.K, g.ldb, 128);
+  PairParams p;
+  const int unit = g.epi == EPI_RELU2_FP8 ? 16 : g.epi == EPI_STORE_F32 ? 4 : 8;  // values in 16 bytes
+  p.n_tma = g.N / unit * unit;
+  const int64_t cols = max(p.n_tma, unit);  // a D narrower than a unit leaves without the map
+  if (g.epi == EPI_RELU2_FP8) {
+    ok = ok && make_map8(&md, g.D, g.M, cols, g.ldd, 32);
+  } else if (g.epi == EPI_STORE_F32) {
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)g.M}, strides[1] = {(cuuint64_t)g.ldd * 4};
+    const cuuint32_t box[2] = {32, 32}, estr[2] = {1, 1};
+    ok = ok && encode_fn()(&md, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, g.D, dims, strides, box, estr,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  } else {
+    ok = ok && make_map(&md, g.D, g.M, cols, g.ldd, 64, 32);
+  }
+  if (!ok) return cudaErrorInvalidValue;
+  p.D = g.D; p.ldd = g.ldd;
+  p.M = g.M; p.N = g.N; p.kblocks = (g.K + BK - 1) / BK;
+  p.n_m = (g.M + 255) / 256;
+  p.n_n = (g.N + 255) / 256;
+  if ((int64_t)p.n_m * p.n_n > INT32_MAX / 2) return cudaErrorInvalidValue;  // unit + grid stays an int
+  p.units = p.n_m * p.n_n;
+  p.sa = g.sa; p.lsa = g.lsa; p.sb = g.sb; p.lsb = g.lsb; p.sd = g.sd; p.lsd = g.lsd;
+  p.epi = g.epi; p.status = status;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * min(p.units, num_sms / 2));
+  cfg.blockDim = dim3(PTHREADS);
+  cfg.dynamicSmemBytes = PSMEM;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, gemm_fp8_pair_kernel, ma, mb, md, p);
+}
+
 inline cudaError_t init() {
   cudaError_t e = tc_init();
   auto big = [&](auto *k, int bytes) {
@@ -361,13 +795,17 @@ inline cudaError_t init() {
   big(gemm_fp8_rows_kernel<32>, RowsCfg<32>::kSmem);
   big(gemm_fp8_rows_kernel<64>, RowsCfg<64>::kSmem);
   big(gemm_fp8_rows_kernel<128>, RowsCfg<128>::kSmem);
+  big(gemm_fp8_pair_kernel, PSMEM);
+  cudaFuncAttributes a;
+  if (e == cudaSuccess) e = cudaFuncGetAttributes(&a, gemm_fp8_pair_kernel);
+  if (e == cudaSuccess && a.numRegs != PREGS) e = cudaErrorInvalidConfiguration;  // the register split would not add up
   return e;
 }
 
 }  // namespace tc8
 
 inline cudaError_t launch_gemm_fp8(const GemmFp8Problem &g, int num_sms, int *status, cudaStream_t st) {
-  (void)num_sms;
+  if (g.M > 256) return tc8::launch_pair(g, num_sms, status, st);
   if (g.M <= 16) return tc8::launch_rows<16>(g, status, st);
   if (g.M <= 32) return tc8::launch_rows<32>(g, status, st);
   if (g.M <= 64) return tc8::launch_rows<64>(g, status, st);

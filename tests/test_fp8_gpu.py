@@ -348,7 +348,10 @@ SHAPES = [
     # M, N, K
     (1, 1, 1), (1, 16, 128), (1, 1536, 1280), (2, 130, 272), (16, 1000, 640), (17, 257, 1040), (32, 128, 144),
     (33, 300, 2048), (64, 129, 384), (65, 513, 512), (127, 128, 4096), (128, 640, 1280), (129, 64, 48),
-    (200, 1003, 656), (300, 520, 1040), (515, 776, 1296), (1030, 264, 272),
+    (200, 1003, 656), (300, 520, 1040), (515, 776, 1296), (1030, 264, 272), (270, 200, 8208),
+    (20485, 392, 272),     # several tiles per pair of CTAs, the last column half of 8 columns
+    (300, 1003, 272), (290, 5, 144), (513, 385, 130), (300, 262, 16),   # N that no 16-byte unit divides
+    (40, 20485, 144),      # many weight tiles
 ]
 
 
