@@ -30,6 +30,9 @@ __device__ __forceinline__ uint32_t cvt2(float lo, float hi) {
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
   return r;
 }
+__device__ __forceinline__ uint32_t cvt4(float a, float b, float c, float d) {
+  return cvt2(a, b) | (cvt2(c, d) << 16);
+}
 
 // What turns a block's values into codes, from the block's largest magnitude
 // a.  Blocks below 2^-100 are scaled up by 2^100 first (exact), because

@@ -70,6 +70,13 @@ __device__ __forceinline__ void tmem_wait16(uint32_t (&r)[16]) {
                  "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
 }
 
+// relu that keeps a NaN
+__device__ __forceinline__ float relu_nan(float x) {
+  float y;
+  asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // 15 tanh(z / 15) from one exponential: t = (1 - E) / (1 + E), E = exp(-2 |z| / 15)
 __device__ __forceinline__ float softcap8(float z) {
   const float e = __expf(-2.f / kSoftcap * fabsf(z));
@@ -124,8 +131,8 @@ __device__ __forceinline__ void rows_store(const RowsParams &p, int m, int n, fl
   if (p.epi == EPI_RELU2 || p.epi == EPI_RELU2_FP8) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float t = v[j] < 0.f ? 0.f : v[j];  // NaN stays
-      v[j] = t * t;
+      v[j] = relu_nan(v[j]);
+      v[j] *= v[j];
     }
   } else if (p.epi == EPI_SOFTCAP) {
 #pragma unroll
@@ -139,7 +146,7 @@ __device__ __forceinline__ void rows_store(const RowsParams &p, int m, int n, fl
     a = warp_max(a);
     const fp8::Quant z(a);
     const float f = z.inv, pre = z.pre;
-    const uint32_t c = fp8::cvt2(v[0] * pre * f, v[1] * pre * f) | (fp8::cvt2(v[2] * pre * f, v[3] * pre * f) << 16);
+    const uint32_t c = fp8::cvt4(v[0] * pre * f, v[1] * pre * f, v[2] * pre * f, v[3] * pre * f);
     uint8_t *d = reinterpret_cast<uint8_t *>(p.D) + (int64_t)m * p.ldd + n;
     if (left >= 4) *reinterpret_cast<uint32_t *>(d) = c;
     else
@@ -339,9 +346,7 @@ __global__ void __launch_bounds__(RowsCfg<TN>::kThreads, 2)
 // TMEM holds two 256-column accumulators, one K block each: while the tensor
 // cores fill one, the eight epilogue warps of each CTA scale and add the other
 // into fp32 sums in registers (thread = one row x 128 columns: one weight
-// block, so one scale per thread and K block).  Per K block and SM the MMAs
-// take 512 cycles at the full rate, the TMEM reads 256 and the packed
-// multiply-adds 128 issue slots per scheduler: the tensor pipe stays the bound.
+// block, so one scale per thread and K block).
 // A thread's 128 columns are also one 1 x 128 output block, so the 8-bit
 // epilogue finds its maximum without leaving the thread.
 //
@@ -392,6 +397,37 @@ __device__ __forceinline__ void pair_tail(const PairParams &p, uint8_t *my, int 
   }
 }
 
+// the wait for tmem_ld32_nw, its registers passed through it
+__device__ __forceinline__ void tmem_wait32(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
+}
+// Arrive on the barrier at this offset in CTA `rank`, without release
+// semantics: what it hands over is TMEM whose reads have completed
+// (tcgen05.wait::ld returned their values).  A releasing arrive at cluster
+// scope first waits for the thread's global loads (the scales fetched ahead):
+// measured 596 against 341 us at 16384 x 2048 x 8192.
+__device__ __forceinline__ void mbar_arrive_remote_relaxed(uint32_t bar, uint32_t rank) {
+  asm volatile(
+      "{\n\t.reg .b32 ra;\n\t"
+      "mapa.shared::cluster.u32 ra, %0, %1;\n\t"
+      "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [ra];\n\t}" ::"r"(bar),
+      "r"(rank)
+      : "memory");
+}
+
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t e;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(e));
+  return e;
+}
 __device__ __forceinline__ void mma8_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                           uint32_t accumulate) {
   asm volatile(
@@ -423,30 +459,29 @@ __global__ void __launch_bounds__(PTHREADS, 1)
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t *staging = smem + S * PSTAGE_BYTES;
   uint64_t *bars = reinterpret_cast<uint64_t *>(staging + PEPI_WARPS * 2 * PBOX);
-  // bars: full[S], empty[S], tfull[2], tempty[2], drain, aux[PEPI_WARPS]
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * S + 5 + PEPI_WARPS);
+  // bars: full[S], done[S], tempty[2], drain, aux[PEPI_WARPS]
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * S + 3 + PEPI_WARPS);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-  static_assert((2 * S + 5 + PEPI_WARPS) * 8 + 8 <= 256, "barriers, TMEM slot and abort flag fit their 256 bytes");
+  static_assert((2 * S + 3 + PEPI_WARPS) * 8 + 8 <= 256, "barriers, TMEM slot and abort flag fit their 256 bytes");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const bool leader = rank == 0;
   const int cluster = blockIdx.x >> 1, n_clusters = gridDim.x >> 1;
   auto full_bar = [&](int s) { return smem_u32(bars + s); };
-  auto empty_bar = [&](int s) { return smem_u32(bars + S + s); };
-  auto tfull_bar = [&](int a) { return smem_u32(bars + 2 * S + a); };
-  auto tempty_bar = [&](int a) { return smem_u32(bars + 2 * S + 2 + a); };
-  const uint32_t drain_bar = smem_u32(bars + 2 * S + 4);
-  auto aux_bar = [&](int w) { return smem_u32(bars + 2 * S + 5 + w); };
+  // done[s]: the MMAs on stage s are complete, so the stage is free and its
+  // accumulator full.  (The epilogue cannot miss a phase: the stage's next
+  // MMAs wait for an accumulator that it has yet to hand back.)
+  auto done_bar = [&](int s) { return smem_u32(bars + S + s); };
+  auto tempty_bar = [&](int a) { return smem_u32(bars + 2 * S + a); };
+  const uint32_t drain_bar = smem_u32(bars + 2 * S + 2);
+  auto aux_bar = [&](int w) { return smem_u32(bars + 2 * S + 3 + w); };
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(full_bar(s), 1);
-      mbar_init(empty_bar(s), 1);
+      mbar_init(done_bar(s), 1);
     }
-    for (int a = 0; a < 2; ++a) {
-      mbar_init(tfull_bar(a), 1);
-      mbar_init(tempty_bar(a), 2 * PEPI_WARPS);  // both CTAs' epilogue warps
-    }
+    for (int a = 0; a < 2; ++a) mbar_init(tempty_bar(a), 2 * PEPI_WARPS);  // both CTAs' epilogue warps
     mbar_init(drain_bar, 1);
     for (int w = 0; w < PEPI_WARPS; ++w) mbar_init(aux_bar(w), 1);
     *abort_flag = 0;
@@ -477,7 +512,7 @@ __global__ void __launch_bounds__(PTHREADS, 1)
         pair_tile(p, u, m_blk, n_blk);
         const int m_row = m_blk * 256 + (int)rank * 128, n_row = n_blk * 256 + (int)rank * 128;
         for (int kb = 0; kb < p.kblocks; ++kb) {
-          if (!mbar_wait<true>(empty_bar(stage), phase ^ 1, abort_flag, p.status)) { ok = false; break; }
+          if (!mbar_wait<true>(done_bar(stage), phase ^ 1, abort_flag, p.status)) { ok = false; break; }
           const uint32_t sa = smem_u32(smem + stage * PSTAGE_BYTES);
           if (leader) mbar_expect_tx(full_bar(stage), 2 * PSTAGE_BYTES);
           const uint32_t fb = cluster_addr(full_bar(stage), 0);
@@ -497,34 +532,42 @@ __global__ void __launch_bounds__(PTHREADS, 1)
         }
     }
   } else if (warp == 1) {
-    if (lane == 0 && leader) {
+    if (leader) {
       // ---------------- MMA issuer ----------------
+      // The warp stays converged and one elected lane issues, so descriptors
+      // are computed in uniform registers (measured below).
       const uint32_t idesc = idesc8(256, 256);
+      const uint32_t elected = elect_one();
+      const uint64_t desc0 = smem_desc(smem_u32(smem), 16, 1024);
       int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
       for (int u = cluster; u < p.units && ok; u += n_clusters) {
         for (int kb = 0; kb < p.kblocks; ++kb) {
-          if (!mbar_wait<true>(tempty_bar(acc), acc_phase ^ 1, abort_flag, p.status) ||
-              !mbar_wait<true>(full_bar(stage), phase, abort_flag, p.status)) {
-            ok = false;
-            break;
-          }
+          ok = mbar_wait(full_bar(stage), phase, abort_flag, p.status) &&
+               mbar_wait(tempty_bar(acc), acc_phase ^ 1, abort_flag, p.status);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
           tc_fence_after();
-          const uint32_t sa = smem_u32(smem + stage * PSTAGE_BYTES), sb = sa + 128 * BK;
+          const uint64_t ad = desc0 + (uint64_t)(stage * (PSTAGE_BYTES >> 4)), bd = ad + (128 * BK >> 4);
+          if (elected) {
 #pragma unroll
-          for (int kk = 0; kk < BK / 32; ++kk)
-            mma8_pair(tmem_base + acc * 256, smem_desc(sa + kk * 32, 16, 1024), smem_desc(sb + kk * 32, 16, 1024), idesc,
-                      kk > 0);
-          tc_commit_pair(empty_bar(stage), 0x3);
-          tc_commit_pair(tfull_bar(acc), 0x3);
+            for (int kk = 0; kk < BK / 32; ++kk)
+              mma8_pair(tmem_base + acc * 256, ad + 2 * kk, bd + 2 * kk, idesc, kk > 0);
+            tc_commit_pair(done_bar(stage), 0x3);
+          }
+          __syncwarp();
           if (++stage == S) { stage = 0; phase ^= 1; }
-          if (++acc == 2) { acc = 0; acc_phase ^= 1; }
+          acc ^= 1;
+          if (acc == 0) acc_phase ^= 1;
         }
       }
-      tc_commit_pair(drain_bar, 0x1);
-      const uint64_t t0 = globaltimer();
-      while (!mbar_try(drain_bar, 0) && globaltimer() - t0 < kWaitNs) {}
+      if (elected) {
+        tc_commit_pair(drain_bar, 0x1);
+        const uint64_t t0 = globaltimer();
+        while (!mbar_try(drain_bar, 0) && globaltimer() - t0 < kWaitNs) {}
+      }
+      __syncwarp();
     }
   }
   } else {
@@ -538,18 +581,28 @@ __global__ void __launch_bounds__(PTHREADS, 1)
     const uint32_t aux = aux_bar(warp - 4);
     uint32_t aux_phase = 0;
     bool aux_inflight = false;
-    int acc = 0;
-    uint32_t acc_phase = 0;
+    int acc = 0, stage = 0;
+    uint32_t phase = 0;
     bool ok = true;
-    // this thread's scale of K block kb in unit u
-    auto scale_of = [&](int u, int kb) {
+    // This thread's two scales of K blocks kb and kb + 1, fetched two blocks
+    // ahead (a block takes less time than a load from L2).  Rows and columns
+    // outside the matrix take the scales of the last one inside; they are not stored.
+    constexpr int AHEAD = 2;
+    float fa[AHEAD], fb[AHEAD];
+    const float *pa = nullptr, *pb = nullptr;
+    auto first_scales = [&](int u) {
       int m_blk, n_blk;
       pair_tile(p, u, m_blk, n_blk);
-      const int m = m_blk * 256 + (int)rank * 128 + quarter * 32 + lane, nb = n_blk * 2 + cg;
-      if (m >= p.M || nb * 128 >= p.N) return 0.f;
-      return p.sa[(int64_t)kb * p.lsa + m] * p.sb[(int64_t)nb * p.lsb + kb];
+      pa = p.sa + min(m_blk * 256 + (int)rank * 128 + quarter * 32 + lane, p.M - 1);
+      pb = p.sb + (int64_t)min(n_blk * 2 + cg, (p.N - 1) >> 7) * p.lsb;
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) {
+        const int kb = min(i, p.kblocks - 1);
+        fa[i] = pa[kb * p.lsa];
+        fb[i] = pb[kb];
+      }
     };
-    float next = cluster < p.units ? scale_of(cluster, 0) : 0.f;
+    if (cluster < p.units) first_scales(cluster);
     for (int u = cluster; u < p.units; u += n_clusters) {
       int m_blk, n_blk;
       pair_tile(p, u, m_blk, n_blk);
@@ -567,34 +620,46 @@ __global__ void __launch_bounds__(PTHREADS, 1)
       uint64_t sum[64];
 #pragma unroll
       for (int i = 0; i < 64; ++i) sum[i] = 0;
-      for (int kb = 0; kb < p.kblocks; ++kb) {
-        const uint64_t f = f2(next, next);
-        // the next block's scale, or the next tile's first
-        if (kb + 1 < p.kblocks) next = scale_of(u, kb + 1);
-        else if (u + n_clusters < p.units) next = scale_of(u + n_clusters, 0);
-        ok = __all_sync(0xffffffffu, mbar_wait<true>(tfull_bar(acc), acc_phase, abort_flag, p.status));
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t t = t_row + acc * 256;
-        uint32_t v[2][16];
-        tmem_ld16_nw(t, v[0]);
+      for (int kb0 = 0; kb0 < p.kblocks && ok; kb0 += AHEAD) {
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          tmem_wait16(v[c & 1]);
-          if (c < 7) tmem_ld16_nw(t + 16 * (c + 1), v[(c + 1) & 1]);
+        for (int i = 0; i < AHEAD; ++i) {
+          const int kb = kb0 + i;
+          if (kb >= p.kblocks) break;
+          ok = __all_sync(0xffffffffu, mbar_wait(done_bar(stage), phase, abort_flag, p.status));
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t t = t_row + acc * 256;
+          uint32_t v[2][32];
+          tmem_ld32_nw(t, v[0]);
+          const float s = fa[i] * fb[i];
+          const uint64_t f = f2(s, s);
+          if (kb + AHEAD < p.kblocks) {
+            fa[i] = pa[(kb + AHEAD) * p.lsa];
+            fb[i] = pb[kb + AHEAD];
+          }
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            sum[8 * c + j] = fma2(f2(__uint_as_float(v[c & 1][2 * j]), __uint_as_float(v[c & 1][2 * j + 1])), f,
-                                  sum[8 * c + j]);
+          for (int c = 0; c < 4; ++c) {
+            tmem_wait32(v[c & 1]);
+            if (c < 3) {
+              tmem_ld32_nw(t + 32 * (c + 1), v[(c + 1) & 1]);
+            } else {  // all read: the accumulator goes back before the last sums
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) {
+                if (leader) mbar_arrive(tempty_bar(acc));
+                else mbar_arrive_remote_relaxed(tempty_bar(acc), 0);
+              }
+            }
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              sum[16 * c + j] = fma2(f2(__uint_as_float(v[c & 1][2 * j]), __uint_as_float(v[c & 1][2 * j + 1])), f,
+                                     sum[16 * c + j]);
+          }
+          acc ^= 1;
+          if (++stage == S) { stage = 0; phase ^= 1; }
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          if (leader) mbar_arrive(tempty_bar(acc));
-          else mbar_arrive_remote(tempty_bar(acc), 0);
-        }
-        if (++acc == 2) { acc = 0; acc_phase ^= 1; }
       }
+      if (u + n_clusters < p.units) first_scales(u + n_clusters);
       if (!ok) break;
       if (!mine) continue;
       if (p.epi == EPI_ADD && by_tma) {
@@ -640,23 +705,27 @@ __global__ void __launch_bounds__(PTHREADS, 1)
         for (int i = 0; i < 64; ++i) {
           float lo, hi;
           f2split(sum[i], lo, hi);
-          lo = lo < 0.f ? 0.f : lo;
-          hi = hi < 0.f ? 0.f : hi;
-          sum[i] = mul2(f2(lo, hi), f2(lo, hi));
+          sum[i] = f2(relu_nan(lo), relu_nan(hi));
+          sum[i] = mul2(sum[i], sum[i]);
           f2split(sum[i], lo, hi);
-          a = fmaxf(a, fmaxf(lo, hi));
+          a = max3(a, lo, hi);
         }
         const fp8::Quant z(a);
-        const uint64_t f = f2(z.inv, z.inv), pre = f2(z.pre, z.pre);
+        const uint64_t f = f2(z.inv, z.inv);
+        if (__any_sync(0xffffffffu, z.pre != 1.f)) {  // a tiny row is scaled up first
+          const uint64_t pre = f2(z.pre, z.pre);
+#pragma unroll
+          for (int i = 0; i < 64; ++i) sum[i] = mul2(sum[i], pre);
+        }
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
           uint32_t w[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             float o[4];
-            f2split(mul2(mul2(sum[8 * q + 2 * j], pre), f), o[0], o[1]);
-            f2split(mul2(mul2(sum[8 * q + 2 * j + 1], pre), f), o[2], o[3]);
-            w[j] = fp8::cvt2(o[0], o[1]) | (fp8::cvt2(o[2], o[3]) << 16);
+            f2split(mul2(sum[8 * q + 2 * j], f), o[0], o[1]);
+            f2split(mul2(sum[8 * q + 2 * j + 1], f), o[2], o[3]);
+            w[j] = fp8::cvt4(o[0], o[1], o[2], o[3]);
           }
           *reinterpret_cast<uint4 *>(my + ((q ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
         }
@@ -678,8 +747,8 @@ __global__ void __launch_bounds__(PTHREADS, 1)
           } else if (p.epi == EPI_RELU2) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-              const float t = o[j] < 0.f ? 0.f : o[j];
-              o[j] = t * t;
+              o[j] = relu_nan(o[j]);
+              o[j] *= o[j];
             }
           } else if (p.epi == EPI_SOFTCAP) {
 #pragma unroll
