@@ -90,24 +90,31 @@ __device__ __forceinline__ float softcap8(float z) {
 //
 // Roles: warp 0 TMA, warp 1 MMA, the others add up (thread = weight row, up
 // to 64 activation rows in registers).
+//
+// Few tiles leave SMs idle, so K is cut over a cluster of 1, 2, 4 or 8 CTAs:
+// each leaves its sums in its own shared memory, and each then adds the
+// cluster's sums of every splits-th activation row, in rank order (the bits
+// do not depend on which CTA ends first), and stores them.
 template <int TN> struct RowsCfg {
   static constexpr int kEpiWarps = TN > 64 ? 8 : 4;        // 4 cover the 128 TMEM lanes; 8: two column halves
   static constexpr int kCols = TN * 4 / kEpiWarps;         // activation rows per thread
   static constexpr int kThreads = 64 + 32 * kEpiWarps;
   static constexpr int kStageBytes = (128 + TN) * BK;
-  static constexpr int kStages = TN == 16 ? 6 : TN == 32 ? 5 : TN == 64 ? 4 : 3;
-  static constexpr int kAccs = TN > 64 ? 2 : 4;            // TMEM accumulators in flight
-  static constexpr int kTmemCols = kAccs * TN;             // 64, 128, 256, 256: a power of two
+  static constexpr int kCtas = TN > 64 ? 1 : 2;            // per SM
+  static constexpr int kStages = TN == 32 ? 5 : TN == 64 ? 4 : 6;
+  static constexpr int kAccs = 4;                          // TMEM accumulators in flight
+  static constexpr int kTmemCols = kAccs * TN;             // 64, 128, 256, 512: a power of two
   static constexpr int kScaleBytes = kEpiWarps * kCols * 4;
   static constexpr int kSmem = kStages * kStageBytes + kScaleBytes + 256 + 1024;
   static_assert(TN * 128 * 4 <= kStages * kStageBytes, "the sums of a tile fit the ring");
-  // two CTAs share an SM and no third fits, so their TMEM always does
-  static_assert(2 * kSmem <= 232448 && 3 * kSmem > 232448 && 2 * kTmemCols <= 512, "two CTAs per SM");
+  // no more CTAs fit an SM than its TMEM serves: an allocation never waits for another CTA's
+  static_assert(kCtas * (kSmem + 1024) <= 233472 && (kCtas + 1) * (kSmem + 1024) > 233472 && kCtas * kTmemCols <= 512,
+                "CTAs per SM");
 };
 
 struct RowsParams {
   int M, N, kblocks;
-  int n_m, n_n;
+  int n_m, splits;      // CTAs per cluster
   const float *sa, *sb;
   int64_t lsa, lsb;
   void *D;
@@ -169,8 +176,17 @@ __device__ __forceinline__ void rows_store(const RowsParams &p, int m, int n, fl
   }
 }
 
+__device__ __forceinline__ float4 ld_cluster(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
 template <int TN>
-__global__ void __launch_bounds__(RowsCfg<TN>::kThreads, 2)
+__global__ void __launch_bounds__(RowsCfg<TN>::kThreads, RowsCfg<TN>::kCtas)
     gemm_fp8_rows_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
                          const RowsParams p) {
   using Cfg = RowsCfg<TN>;
@@ -189,10 +205,12 @@ __global__ void __launch_bounds__(RowsCfg<TN>::kThreads, 2)
   auto tfull_bar = [&](int a) { return smem_u32(bars + 2 * S + a); };
   auto tempty_bar = [&](int a) { return smem_u32(bars + 2 * S + NA + a); };
   const uint32_t drain_bar = smem_u32(bars + 2 * S + 2 * NA);
-  const int m0 = (int)(blockIdx.x % p.n_m) * TN;
-  const int nb = blockIdx.x / p.n_m;
+  // tiles of one weight row block are neighbours, so its panel is read from L2 after the first
+  const int rank = (int)(blockIdx.x % p.splits), tile = blockIdx.x / p.splits;
+  const int m0 = tile % p.n_m * TN;
+  const int nb = tile / p.n_m;
   const int n0 = nb * 128;
-  const int kb0 = 0, kb1 = p.kblocks;
+  const int kb0 = (int)((int64_t)p.kblocks * rank / p.splits), kb1 = (int)((int64_t)p.kblocks * (rank + 1) / p.splits);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
@@ -219,7 +237,7 @@ __global__ void __launch_bounds__(RowsCfg<TN>::kThreads, 2)
       int stage = 0, issued = 0;
       uint32_t phase = 0;
       for (int kb = kb0; kb < kb1; ++kb) {
-        if (!mbar_wait<true>(empty_bar(stage), phase ^ 1, abort_flag, p.status)) break;
+        if (!mbar_wait(empty_bar(stage), phase ^ 1, abort_flag, p.status)) break;
         const uint32_t sw = smem_u32(smem + stage * Cfg::kStageBytes);
         mbar_expect_tx(full_bar(stage), Cfg::kStageBytes);
         tma_load_2d(sw, &map_w, kb * BK, n0, full_bar(stage));
@@ -241,8 +259,8 @@ __global__ void __launch_bounds__(RowsCfg<TN>::kThreads, 2)
       int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
       for (int kb = kb0; kb < kb1; ++kb) {
-        if (!mbar_wait<true>(tempty_bar(acc), acc_phase ^ 1, abort_flag, p.status)) break;
-        if (!mbar_wait<true>(full_bar(stage), phase, abort_flag, p.status)) break;
+        if (!mbar_wait(tempty_bar(acc), acc_phase ^ 1, abort_flag, p.status)) break;
+        if (!mbar_wait(full_bar(stage), phase, abort_flag, p.status)) break;
         tc_fence_after();
         const uint32_t sw = smem_u32(smem + stage * Cfg::kStageBytes);
         const uint32_t sx = sw + 128 * BK;
@@ -270,45 +288,46 @@ __global__ void __launch_bounds__(RowsCfg<TN>::kThreads, 2)
     for (int i = 0; i < COLS / 2; ++i) sum[i] = 0;
     // lane l fetches the scales of activation rows l, l + 32, one K block ahead
     constexpr int NS = (COLS + 31) / 32;
-    auto fetch = [&](int kb, float (&f)[NS]) {
-      const float wb = kb < kb1 ? p.sb[(int64_t)nb * p.lsb + kb] : 0.f;
+    float fa[NS], fb = 0.f;
+    auto fetch = [&](int kb) {
+      fb = p.sb[(int64_t)nb * p.lsb + kb];
 #pragma unroll
       for (int i = 0; i < NS; ++i) {
         const int c = lane + 32 * i, m = m0 + c0 + c;
-        f[i] = (kb < kb1 && c < COLS && m < p.M) ? p.sa[(int64_t)kb * p.lsa + m] * wb : 0.f;
+        fa[i] = (c < COLS && m < p.M) ? p.sa[(int64_t)kb * p.lsa + m] : 0.f;
       }
     };
-    float next[NS];
-    fetch(kb0, next);
+    if (kb0 < kb1) fetch(kb0);
     int acc = 0;
     uint32_t acc_phase = 0;
     for (int kb = kb0; kb < kb1; ++kb) {
       __syncwarp();  // the previous block's scales have been read
 #pragma unroll
       for (int i = 0; i < NS; ++i)
-        if (lane + 32 * i < COLS) sw[lane + 32 * i] = next[i];
+        if (lane + 32 * i < COLS) sw[lane + 32 * i] = fa[i] * fb;
       __syncwarp();
-      fetch(kb + 1, next);
-      const bool ok = mbar_wait<true>(tfull_bar(acc), acc_phase, abort_flag, p.status);
+      if (kb + 1 < kb1) fetch(kb + 1);
+      const bool ok = mbar_wait(tfull_bar(acc), acc_phase, abort_flag, p.status);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
       const uint32_t t = tmem_base + ((uint32_t)(quarter * 32) << 16) + acc * TN + c0;
+      uint32_t v[COLS / 16][16];
 #pragma unroll
-      for (int c = 0; c < COLS; c += 16) {
-        uint32_t v[16];
-        tmem_ld16_nw(t + c, v);
-        tmem_wait16(v);
+      for (int c = 0; c < COLS / 16; ++c) tmem_ld16_nw(t + 16 * c, v[c]);
 #pragma unroll
-        for (int j = 0; j < 16; j += 4) {
-          const float4 f = *reinterpret_cast<const float4 *>(sw + c + j);
-          sum[(c + j) / 2] = fma2(f2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), f2(f.x, f.y), sum[(c + j) / 2]);
-          sum[(c + j) / 2 + 1] =
-              fma2(f2(__uint_as_float(v[j + 2]), __uint_as_float(v[j + 3])), f2(f.z, f.w), sum[(c + j) / 2 + 1]);
-        }
-      }
+      for (int c = 0; c < COLS / 16; ++c) tmem_wait16(v[c]);  // the first waits for all
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(tempty_bar(acc));
+#pragma unroll
+      for (int c = 0; c < COLS / 16; ++c)
+#pragma unroll
+        for (int j = 0; j < 16; j += 4) {
+          const float4 f = *reinterpret_cast<const float4 *>(sw + 16 * c + j);
+          uint64_t *o = sum + 8 * c + j / 2;
+          o[0] = fma2(f2(__uint_as_float(v[c][j]), __uint_as_float(v[c][j + 1])), f2(f.x, f.y), o[0]);
+          o[1] = fma2(f2(__uint_as_float(v[c][j + 2]), __uint_as_float(v[c][j + 3])), f2(f.z, f.w), o[1]);
+        }
       if (++acc == NA) { acc = 0; acc_phase ^= 1; }
     }
     // The last accumulator is complete, so every MMA has read the ring and
@@ -329,12 +348,18 @@ __global__ void __launch_bounds__(RowsCfg<TN>::kThreads, 2)
   __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem_base, Cfg::kTmemCols);
+  if (p.splits > 1) cluster_sync_all();  // every CTA's sums are in its shared memory
   // one warp per activation row: 128 weight rows are one 1 x 128 output block
-  for (int c = warp; c < TN && m0 + c < p.M; c += Cfg::kThreads / 32) {
-    const float4 f = *reinterpret_cast<const float4 *>(smem + (c * 128 + lane * 4) * 4);
-    float v[4] = {f.x, f.y, f.z, f.w};
+  for (int c = rank + warp * p.splits; c < TN && m0 + c < p.M; c += Cfg::kThreads / 32 * p.splits) {
+    const uint32_t at = smem_u32(smem) + (c * 128 + lane * 4) * 4;
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int r = 0; r < p.splits; ++r) {
+      const float4 f = ld_cluster(cluster_addr(at, r));
+      v[0] += f.x; v[1] += f.y; v[2] += f.z; v[3] += f.w;
+    }
     rows_store(p, m0 + c, n0 + lane * 4, v, lane);
   }
+  if (p.splits > 1) cluster_sync_all();  // no CTA leaves while its sums are read
 }
 
 // ===========================================================================
@@ -798,19 +823,33 @@ inline bool make_map8(CUtensorMap *map, const void *base, int64_t rows, int64_t 
 }
 
 template <int TN>
-inline cudaError_t launch_rows(const GemmFp8Problem &g, int *status, cudaStream_t st) {
+inline cudaError_t launch_rows(const GemmFp8Problem &g, int num_sms, int *status, cudaStream_t st) {
   using Cfg = RowsCfg<TN>;
   CUtensorMap mw, mx;
   if (!make_map8(&mw, g.B, g.N, g.K, g.ldb, 128) || !make_map8(&mx, g.A, g.M, g.K, g.lda, TN)) return cudaErrorInvalidValue;
   RowsParams p;
   p.M = g.M; p.N = g.N; p.kblocks = (g.K + BK - 1) / BK;
   p.n_m = (g.M + TN - 1) / TN;
-  p.n_n = (g.N + 127) / 128;
   p.sa = g.sa; p.lsa = g.lsa; p.sb = g.sb; p.lsb = g.lsb;
   p.D = g.D; p.ldd = g.ldd; p.sd = g.sd; p.lsd = g.lsd; p.epi = g.epi; p.status = status;
-  if ((int64_t)p.n_m * p.n_n > INT32_MAX) return cudaErrorInvalidValue;
-  gemm_fp8_rows_kernel<TN><<<p.n_m * p.n_n, Cfg::kThreads, Cfg::kSmem, st>>>(mw, mx, p);
-  return cudaGetLastError();
+  const int64_t tiles = (int64_t)p.n_m * ((g.N + 127) / 128);
+  // cut K while every CTA still finds a place at once and keeps a K block
+  p.splits = 1;
+  while (p.splits < 8 && 2 * p.splits <= p.kblocks && tiles * 2 * p.splits <= Cfg::kCtas * num_sms) p.splits *= 2;
+  if (tiles * p.splits > INT32_MAX) return cudaErrorInvalidValue;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(tiles * p.splits));
+  cfg.blockDim = dim3(Cfg::kThreads);
+  cfg.dynamicSmemBytes = Cfg::kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = p.splits;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.splits > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, gemm_fp8_rows_kernel<TN>, mw, mx, p);
 }
 
 inline cudaError_t launch_pair(const GemmFp8Problem &g, int num_sms, int *status, cudaStream_t st) {
@@ -874,11 +913,17 @@ inline cudaError_t init() {
 }  // namespace tc8
 
 inline cudaError_t launch_gemm_fp8(const GemmFp8Problem &g, int num_sms, int *status, cudaStream_t st) {
-  if (g.M > 256) return tc8::launch_pair(g, num_sms, status, st);
-  if (g.M <= 16) return tc8::launch_rows<16>(g, status, st);
-  if (g.M <= 32) return tc8::launch_rows<32>(g, status, st);
-  if (g.M <= 64) return tc8::launch_rows<64>(g, status, st);
-  return tc8::launch_rows<128>(g, status, st);
+#ifndef PAIRM
+#define PAIRM 256
+#endif
+  if (g.M > PAIRM) return tc8::launch_pair(g, num_sms, status, st);
+  if (g.M <= 16) return tc8::launch_rows<16>(g, num_sms, status, st);
+  if (g.M <= 32) return tc8::launch_rows<32>(g, num_sms, status, st);
+#ifndef M64
+#define M64 64
+#endif
+  if (g.M <= M64) return tc8::launch_rows<64>(g, num_sms, status, st);
+  return tc8::launch_rows<128>(g, num_sms, status, st);
 }
 
 }  // namespace nc
