@@ -55,6 +55,35 @@ __device__ __forceinline__ void mma8(uint32_t d_tmem, uint64_t adesc, uint64_t b
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+// Bounded wait for barriers that are handed over every K block: a count of
+// tries is the limit (a fraction of a second at least), which costs the
+// callers one register where a clock would cost several.
+constexpr uint32_t kTries = 1u << 24;
+__device__ __forceinline__ bool wait8(uint32_t bar, uint32_t parity, volatile int *abort_flag, int *status) {
+  for (uint32_t i = 1; !mbar_try(bar, parity); ++i) {
+    if ((i & 255) == 0 && (*abort_flag || i > kTries)) {
+      if (!*abort_flag) {
+        *abort_flag = 1;
+        set_status(status, kStatusTimeout);
+      }
+      return false;
+    }
+  }
+  return true;
+}
+
+// The warps that issue TMA and MMAs stay converged and one elected lane
+// issues, so descriptors and addresses are computed in uniform registers: four
+// MMAs then issue in 58 cycles, against 310 from a branch that one lane took alone.
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t e;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(e));
+  return e;
+}
 __device__ __forceinline__ void tmem_ld16_nw(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
@@ -91,22 +120,22 @@ __device__ __forceinline__ float softcap8(float z) {
 // Roles: warp 0 TMA, warp 1 MMA, the others add up (thread = weight row, up
 // to 64 activation rows in registers).
 //
-// Few tiles leave SMs idle, so K is cut over a cluster of 1, 2, 4 or 8 CTAs:
-// each leaves its sums in its own shared memory, and each then adds the
-// cluster's sums of every splits-th activation row, in rank order (the bits
-// do not depend on which CTA ends first), and stores them.
+// Few tiles leave SMs idle, so K is cut over a cluster of 1, 2, 4 or 8 CTAs.
+// Each owns TN / splits of the activation rows and receives the others' sums
+// for them in its shared memory; after one cluster barrier it adds them in
+// rank order (the bits do not depend on which CTA ends first) and stores.
 template <int TN> struct RowsCfg {
   static constexpr int kEpiWarps = TN > 64 ? 8 : 4;        // 4 cover the 128 TMEM lanes; 8: two column halves
   static constexpr int kCols = TN * 4 / kEpiWarps;         // activation rows per thread
   static constexpr int kThreads = 64 + 32 * kEpiWarps;
   static constexpr int kStageBytes = (128 + TN) * BK;
   static constexpr int kCtas = TN > 64 ? 1 : 2;            // per SM
-  static constexpr int kStages = TN == 32 ? 5 : TN == 64 ? 4 : 6;
+  static constexpr int kStages = TN == 32 ? 4 : TN == 64 ? 3 : TN == 16 ? 5 : 4;
   static constexpr int kAccs = 4;                          // TMEM accumulators in flight
   static constexpr int kTmemCols = kAccs * TN;             // 64, 128, 256, 512: a power of two
   static constexpr int kScaleBytes = kEpiWarps * kCols * 4;
-  static constexpr int kSmem = kStages * kStageBytes + kScaleBytes + 256 + 1024;
-  static_assert(TN * 128 * 4 <= kStages * kStageBytes, "the sums of a tile fit the ring");
+  static constexpr int kSumBytes = TN * 128 * 4;           // the cluster's sums of this CTA's activation rows
+  static constexpr int kSmem = kStages * kStageBytes + kSumBytes + kScaleBytes + 256 + 1024;
   // no more CTAs fit an SM than its TMEM serves: an allocation never waits for another CTA's
   static_assert(kCtas * (kSmem + 1024) <= 233472 && (kCtas + 1) * (kSmem + 1024) > 233472 && kCtas * kTmemCols <= 512,
                 "CTAs per SM");
@@ -176,13 +205,11 @@ __device__ __forceinline__ void rows_store(const RowsParams &p, int m, int n, fl
   }
 }
 
-__device__ __forceinline__ float4 ld_cluster(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr)
-               : "memory");
-  return v;
+__device__ __forceinline__ void cluster_started(int splits) {
+  if (splits > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void st_cluster(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
 template <int TN>
@@ -193,8 +220,9 @@ __global__ void __launch_bounds__(RowsCfg<TN>::kThreads, RowsCfg<TN>::kCtas)
   constexpr int S = Cfg::kStages, NA = Cfg::kAccs, COLS = Cfg::kCols;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  float *scales = reinterpret_cast<float *>(smem + S * Cfg::kStageBytes);
-  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + S * Cfg::kStageBytes + Cfg::kScaleBytes);
+  float *sums = reinterpret_cast<float *>(smem + S * Cfg::kStageBytes);  // [splits][TN / splits][128]
+  float *scales = sums + Cfg::kSumBytes / 4;
+  uint64_t *bars = reinterpret_cast<uint64_t *>(scales + Cfg::kScaleBytes / 4);
   // bars: full[S], empty[S], tfull[NA], tempty[NA], drain
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * S + 2 * NA + 1);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
@@ -211,19 +239,34 @@ __global__ void __launch_bounds__(RowsCfg<TN>::kThreads, RowsCfg<TN>::kCtas)
   const int nb = tile / p.n_m;
   const int n0 = nb * 128;
   const int kb0 = (int)((int64_t)p.kblocks * rank / p.splits), kb1 = (int)((int64_t)p.kblocks * (rank + 1) / p.splits);
+  const uint32_t elected = warp < 2 ? elect_one() : 0;
 
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < S; ++s) {
-      mbar_init(full_bar(s), 1);
-      mbar_init(empty_bar(s), 1);
+  // waited for before the first store to another CTA: it has started by then
+  if (p.splits > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  if (warp == 0) {
+    if (elected) {
+      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_w)) : "memory");
+      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_x)) : "memory");
+      for (int s = 0; s < S; ++s) {
+        mbar_init(full_bar(s), 1);
+        mbar_init(empty_bar(s), 1);
+      }
+      for (int a = 0; a < NA; ++a) {
+        mbar_init(tfull_bar(a), 1);
+        mbar_init(tempty_bar(a), Cfg::kEpiWarps);
+      }
+      mbar_init(drain_bar, 1);
+      *abort_flag = 0;
+      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+      // the ring's first loads need nothing that the other warps set up
+      for (int s = 0; s < min(S, kb1 - kb0); ++s) {
+        const uint32_t sw = smem_u32(smem + s * Cfg::kStageBytes);
+        mbar_expect_tx(full_bar(s), Cfg::kStageBytes);
+        tma_load_2d(sw, &map_w, (kb0 + s) * BK, n0, full_bar(s));
+        tma_load_2d(sw + 128 * BK, &map_x, (kb0 + s) * BK, m0, full_bar(s));
+      }
     }
-    for (int a = 0; a < NA; ++a) {
-      mbar_init(tfull_bar(a), 1);
-      mbar_init(tempty_bar(a), Cfg::kEpiWarps);
-    }
-    mbar_init(drain_bar, 1);
-    *abort_flag = 0;
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    __syncwarp();
   }
   if (warp == 1) tmem_alloc(smem_u32(tmem_slot), Cfg::kTmemCols);
   tc_fence_before();
@@ -232,51 +275,59 @@ __global__ void __launch_bounds__(RowsCfg<TN>::kThreads, RowsCfg<TN>::kCtas)
   const uint32_t tmem_base = *tmem_slot;
 
   if (warp == 0) {
-    if (lane == 0) {
-      // ---------------- TMA producer ----------------
-      int stage = 0, issued = 0;
-      uint32_t phase = 0;
-      for (int kb = kb0; kb < kb1; ++kb) {
-        if (!mbar_wait(empty_bar(stage), phase ^ 1, abort_flag, p.status)) break;
-        const uint32_t sw = smem_u32(smem + stage * Cfg::kStageBytes);
+    // ---------------- TMA producer ----------------
+    int stage = 0, issued = min(S, kb1 - kb0);
+    uint32_t phase = 1;
+    if (issued < S) { stage = issued; phase = 0; }
+    for (int kb = kb0 + S; kb < kb1; ++kb) {
+      const bool ok = wait8(empty_bar(stage), phase ^ 1, abort_flag, p.status);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      const uint32_t sw = smem_u32(smem + stage * Cfg::kStageBytes);
+      if (elected) {
         mbar_expect_tx(full_bar(stage), Cfg::kStageBytes);
         tma_load_2d(sw, &map_w, kb * BK, n0, full_bar(stage));
         tma_load_2d(sw + 128 * BK, &map_x, kb * BK, m0, full_bar(stage));
-        ++issued;
-        if (++stage == S) { stage = 0; phase ^= 1; }
       }
-      // no copy of ours may still be landing when the CTA exits (bounded)
-      for (int i = 0; i < min(issued, S); ++i) {
-        if (--stage < 0) { stage = S - 1; phase ^= 1; }
-        const uint64_t t0 = globaltimer();
-        while (!mbar_try(full_bar(stage), phase) && globaltimer() - t0 < kWaitNs) {}
-      }
+      __syncwarp();
+      if (++stage == S) { stage = 0; phase ^= 1; }
+    }
+    cluster_started(p.splits);
+    // no copy of ours may still be landing when the CTA exits (bounded)
+    for (int i = 0; i < issued; ++i) {
+      if (--stage < 0) { stage = S - 1; phase ^= 1; }
+      const uint64_t t0 = globaltimer();
+      while (!mbar_try(full_bar(stage), phase) && globaltimer() - t0 < kWaitNs) {}
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      // ---------------- MMA issuer ----------------
-      const uint32_t idesc = idesc8(128, TN);
-      int stage = 0, acc = 0;
-      uint32_t phase = 0, acc_phase = 0;
-      for (int kb = kb0; kb < kb1; ++kb) {
-        if (!mbar_wait(tempty_bar(acc), acc_phase ^ 1, abort_flag, p.status)) break;
-        if (!mbar_wait(full_bar(stage), phase, abort_flag, p.status)) break;
-        tc_fence_after();
-        const uint32_t sw = smem_u32(smem + stage * Cfg::kStageBytes);
-        const uint32_t sx = sw + 128 * BK;
+    // ---------------- MMA issuer ----------------
+    const uint32_t idesc = idesc8(128, TN);
+    const uint64_t desc0 = smem_desc(smem_u32(smem), 16, 1024);
+    int stage = 0, acc = 0;
+    uint32_t phase = 0, acc_phase = 0;
+    for (int kb = kb0; kb < kb1; ++kb) {
+      const bool ok = wait8(tempty_bar(acc), acc_phase ^ 1, abort_flag, p.status) &&
+                      wait8(full_bar(stage), phase, abort_flag, p.status);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc_fence_after();
+      const uint64_t wd = desc0 + (uint64_t)(stage * (Cfg::kStageBytes >> 4)), xd = wd + (128 * BK >> 4);
+      if (elected) {
 #pragma unroll
-        for (int kk = 0; kk < BK / 32; ++kk)
-          mma8(tmem_base + acc * TN, smem_desc(sw + kk * 32, 16, 1024), smem_desc(sx + kk * 32, 16, 1024), idesc, kk > 0);
-        tc_commit(empty_bar(stage));
+        for (int kk = 0; kk < BK / 32; ++kk) mma8(tmem_base + acc * TN, wd + 2 * kk, xd + 2 * kk, idesc, kk > 0);
         tc_commit(tfull_bar(acc));
-        if (++stage == S) { stage = 0; phase ^= 1; }
-        if (++acc == NA) { acc = 0; acc_phase ^= 1; }
+        tc_commit(empty_bar(stage));
       }
-      // every MMA this thread issued has completed once the drain barrier flips
+      __syncwarp();
+      if (++stage == S) { stage = 0; phase ^= 1; }
+      if (++acc == NA) { acc = 0; acc_phase ^= 1; }
+    }
+    cluster_started(p.splits);
+    // every MMA issued has completed once the drain barrier flips
+    if (elected) {
       tc_commit(drain_bar);
       const uint64_t t0 = globaltimer();
       while (!mbar_try(drain_bar, 0) && globaltimer() - t0 < kWaitNs) {}
     }
+    __syncwarp();
   } else {
     // ---------------- sums over the K blocks ----------------
     const int quarter = warp & 3;
@@ -307,7 +358,7 @@ __global__ void __launch_bounds__(RowsCfg<TN>::kThreads, RowsCfg<TN>::kCtas)
         if (lane + 32 * i < COLS) sw[lane + 32 * i] = fa[i] * fb;
       __syncwarp();
       if (kb + 1 < kb1) fetch(kb + 1);
-      const bool ok = mbar_wait(tfull_bar(acc), acc_phase, abort_flag, p.status);
+      const bool ok = wait8(tfull_bar(acc), acc_phase, abort_flag, p.status);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
       const uint32_t t = tmem_base + ((uint32_t)(quarter * 32) << 16) + acc * TN + c0;
@@ -330,36 +381,38 @@ __global__ void __launch_bounds__(RowsCfg<TN>::kThreads, RowsCfg<TN>::kCtas)
         }
       if (++acc == NA) { acc = 0; acc_phase ^= 1; }
     }
-    // The last accumulator is complete, so every MMA has read the ring and
-    // every copy has landed: the ring's memory takes the sums, [activation
-    // row][weight row].  After an abort a copy may still land: no sums then.
-    if (!*abort_flag) {
-      float *red = reinterpret_cast<float *>(smem);
+    cluster_started(p.splits);
+    // to the CTA that owns the activation row
+    const int per = TN / p.splits;  // a power of two
+    const int shift = 31 - __clz(per);
+    const uint32_t to = smem_u32(sums) + (rank * per * 128 + row) * 4;
 #pragma unroll
-      for (int i = 0; i < COLS / 2; ++i) {
+    for (int i = 0; i < COLS; ++i) {
+      const int c = c0 + i;
+      if (m0 + c < p.M) {
         float lo, hi;
-        f2split(sum[i], lo, hi);
-        red[(c0 + 2 * i) * 128 + row] = lo;
-        red[(c0 + 2 * i + 1) * 128 + row] = hi;
+        f2split(sum[i / 2], lo, hi);
+        st_cluster(cluster_addr(to + (c & (per - 1)) * 512, c >> shift), (i & 1) ? hi : lo);
       }
     }
   }
   tc_fence_before();
-  __syncthreads();
+  if (p.splits > 1) cluster_sync_all();  // the cluster's sums have arrived
+  else __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem_base, Cfg::kTmemCols);
-  if (p.splits > 1) cluster_sync_all();  // every CTA's sums are in its shared memory
   // one warp per activation row: 128 weight rows are one 1 x 128 output block
-  for (int c = rank + warp * p.splits; c < TN && m0 + c < p.M; c += Cfg::kThreads / 32 * p.splits) {
-    const uint32_t at = smem_u32(smem) + (c * 128 + lane * 4) * 4;
+  const int per = TN / p.splits;
+  for (int c = warp; c < per && m0 + rank * per + c < p.M; c += Cfg::kThreads / 32) {
+    const float *at = sums + c * 128 + lane * 4;
     float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
     for (int r = 0; r < p.splits; ++r) {
-      const float4 f = ld_cluster(cluster_addr(at, r));
+      const float4 f = *reinterpret_cast<const float4 *>(at + r * per * 128);
       v[0] += f.x; v[1] += f.y; v[2] += f.z; v[3] += f.w;
     }
-    rows_store(p, m0 + c, n0 + lane * 4, v, lane);
+    rows_store(p, m0 + rank * per + c, n0 + lane * 4, v, lane);
   }
-  if (p.splits > 1) cluster_sync_all();  // no CTA leaves while its sums are read
 }
 
 // ===========================================================================
@@ -383,10 +436,10 @@ constexpr int PSTAGE_BYTES = 2 * 128 * BK;  // A and B rows of one CTA: 32 KB
 constexpr int PEPI_WARPS = 8;
 // Three warpgroups: warp 0 TMA, warp 1 MMA (warps 2, 3 idle), warps 4..11 the
 // epilogue, which holds 128 sums a thread.  The first gives registers to the
-// others: 128 x 56 + 256 x 224 = 64,512, all of the 384 x 168 of the launch
+// others: 128 x 24 + 256 x 240 = 64,512, all of the 384 x 168 of the launch
 // (init() checks that count), so every increase can be met.
 constexpr int PTHREADS = 128 + 32 * PEPI_WARPS;
-constexpr int PREGS = 168, PREGS_LOW = 56, PREGS_HIGH = 224;
+constexpr int PREGS = 168, PREGS_LOW = 24, PREGS_HIGH = 240;
 static_assert(128 * PREGS_LOW + 32 * PEPI_WARPS * PREGS_HIGH <= PTHREADS * PREGS, "register split within the launch");
 constexpr int PBOX = 32 * 128;
 constexpr int PSMEM = PSTAGES * PSTAGE_BYTES + PEPI_WARPS * 2 * PBOX + 256 + 1024;
@@ -404,7 +457,6 @@ struct PairParams {
   int64_t lsa, lsb;
   float *sd;
   int64_t lsd;
-  int epi;
   int *status;
 };
 
@@ -422,37 +474,28 @@ __device__ __forceinline__ void pair_tail(const PairParams &p, uint8_t *my, int 
   }
 }
 
-// the wait for tmem_ld32_nw, its registers passed through it
-__device__ __forceinline__ void tmem_wait32(uint32_t (&r)[32]) {
+// the wait for two tmem_ld32_nw; their registers pass through it
+__device__ __forceinline__ void tmem_wait32(uint32_t (&a)[32], uint32_t (&b)[32]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
-                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
-                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
+               : "+r"(a[0]), "+r"(a[1]), "+r"(a[2]), "+r"(a[3]), "+r"(a[4]), "+r"(a[5]), "+r"(a[6]), "+r"(a[7]),
+                 "+r"(a[8]), "+r"(a[9]), "+r"(a[10]), "+r"(a[11]), "+r"(a[12]), "+r"(a[13]), "+r"(a[14]), "+r"(a[15]),
+                 "+r"(a[16]), "+r"(a[17]), "+r"(a[18]), "+r"(a[19]), "+r"(a[20]), "+r"(a[21]), "+r"(a[22]), "+r"(a[23]),
+                 "+r"(a[24]), "+r"(a[25]), "+r"(a[26]), "+r"(a[27]), "+r"(a[28]), "+r"(a[29]), "+r"(a[30]), "+r"(a[31])::"memory");
+  asm volatile(""
+               : "+r"(b[0]), "+r"(b[1]), "+r"(b[2]), "+r"(b[3]), "+r"(b[4]), "+r"(b[5]), "+r"(b[6]), "+r"(b[7]),
+                 "+r"(b[8]), "+r"(b[9]), "+r"(b[10]), "+r"(b[11]), "+r"(b[12]), "+r"(b[13]), "+r"(b[14]), "+r"(b[15]),
+                 "+r"(b[16]), "+r"(b[17]), "+r"(b[18]), "+r"(b[19]), "+r"(b[20]), "+r"(b[21]), "+r"(b[22]), "+r"(b[23]),
+                 "+r"(b[24]), "+r"(b[25]), "+r"(b[26]), "+r"(b[27]), "+r"(b[28]), "+r"(b[29]), "+r"(b[30]), "+r"(b[31]));
 }
-// Arrive on the barrier at this offset in CTA `rank`, without release
-// semantics: what it hands over is TMEM whose reads have completed
+// Arrive on a barrier of the cluster (shared::cluster address) without
+// release semantics: what it hands over is TMEM whose reads have completed
 // (tcgen05.wait::ld returned their values).  A releasing arrive at cluster
 // scope first waits for the thread's global loads (the scales fetched ahead):
 // measured 596 against 341 us at 16384 x 2048 x 8192.
-__device__ __forceinline__ void mbar_arrive_remote_relaxed(uint32_t bar, uint32_t rank) {
-  asm volatile(
-      "{\n\t.reg .b32 ra;\n\t"
-      "mapa.shared::cluster.u32 ra, %0, %1;\n\t"
-      "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [ra];\n\t}" ::"r"(bar),
-      "r"(rank)
-      : "memory");
+__device__ __forceinline__ void mbar_arrive_relaxed(uint32_t bar_cluster) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
 }
 
-__device__ __forceinline__ uint32_t elect_one() {
-  uint32_t e;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "elect.sync _|p, 0xffffffff;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(e));
-  return e;
-}
 __device__ __forceinline__ void mma8_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                           uint32_t accumulate) {
   asm volatile(
@@ -476,6 +519,7 @@ __device__ __forceinline__ void pair_tile(const PairParams &p, int u, int &m_blk
   n_blk = r / size;
 }
 
+template <int EPI>
 __global__ void __launch_bounds__(PTHREADS, 1)
     gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                          const __grid_constant__ CUtensorMap map_d, const PairParams p) {
@@ -484,29 +528,31 @@ __global__ void __launch_bounds__(PTHREADS, 1)
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t *staging = smem + S * PSTAGE_BYTES;
   uint64_t *bars = reinterpret_cast<uint64_t *>(staging + PEPI_WARPS * 2 * PBOX);
-  // bars: full[S], done[S], tempty[2], drain, aux[PEPI_WARPS]
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * S + 3 + PEPI_WARPS);
+  // bars: full[S], done[2 S], tempty[4], drain, aux[PEPI_WARPS]
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 3 * S + 5 + PEPI_WARPS);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-  static_assert((2 * S + 3 + PEPI_WARPS) * 8 + 8 <= 256, "barriers, TMEM slot and abort flag fit their 256 bytes");
+  static_assert((3 * S + 5 + PEPI_WARPS) * 8 + 8 <= 256, "barriers, TMEM slot and abort flag fit their 256 bytes");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const bool leader = rank == 0;
   const int cluster = blockIdx.x >> 1, n_clusters = gridDim.x >> 1;
   auto full_bar = [&](int s) { return smem_u32(bars + s); };
-  // done[s]: the MMAs on stage s are complete, so the stage is free and its
-  // accumulator full.  (The epilogue cannot miss a phase: the stage's next
-  // MMAs wait for an accumulator that it has yet to hand back.)
-  auto done_bar = [&](int s) { return smem_u32(bars + S + s); };
-  auto tempty_bar = [&](int a) { return smem_u32(bars + 2 * S + a); };
-  const uint32_t drain_bar = smem_u32(bars + 2 * S + 2);
-  auto aux_bar = [&](int w) { return smem_u32(bars + 2 * S + 3 + w); };
+  // done[s, h]: the MMAs of stage s and column half h are complete, so that
+  // half of its accumulator is full, and with h = 1, the second, the stage is free.
+  // (The epilogue cannot miss a phase: the stage's next MMAs wait for an
+  // accumulator that it has yet to hand back.)
+  auto done_bar = [&](int s, int h) { return smem_u32(bars + S + 2 * s + h); };
+  auto tempty_bar = [&](int a) { return smem_u32(bars + 3 * S + a); };
+  const uint32_t drain_bar = smem_u32(bars + 3 * S + 4);
+  auto aux_bar = [&](int w) { return smem_u32(bars + 3 * S + 5 + w); };
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(full_bar(s), 1);
-      mbar_init(done_bar(s), 1);
+      mbar_init(done_bar(s, 0), 1);
+      mbar_init(done_bar(s, 1), 1);
     }
-    for (int a = 0; a < 2; ++a) mbar_init(tempty_bar(a), 2 * PEPI_WARPS);  // both CTAs' epilogue warps
+    for (int a = 0; a < 4; ++a) mbar_init(tempty_bar(a), PEPI_WARPS);  // a column half's epilogue warps of both CTAs
     mbar_init(drain_bar, 1);
     for (int w = 0; w < PEPI_WARPS; ++w) mbar_init(aux_bar(w), 1);
     *abort_flag = 0;
@@ -527,41 +573,45 @@ __global__ void __launch_bounds__(PTHREADS, 1)
   if (warp < 4) {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(PREGS_LOW));
   if (warp == 0) {
-    if (lane == 0) {
-      // ---------------- TMA producer ----------------
-      int stage = 0, issued = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      for (int u = cluster; u < p.units && ok; u += n_clusters) {
-        int m_blk, n_blk;
-        pair_tile(p, u, m_blk, n_blk);
-        const int m_row = m_blk * 256 + (int)rank * 128, n_row = n_blk * 256 + (int)rank * 128;
-        for (int kb = 0; kb < p.kblocks; ++kb) {
-          if (!mbar_wait<true>(done_bar(stage), phase ^ 1, abort_flag, p.status)) { ok = false; break; }
-          const uint32_t sa = smem_u32(smem + stage * PSTAGE_BYTES);
+    // ---------------- TMA producer ----------------
+    const uint32_t elected = elect_one();
+    int stage = 0, issued = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int u = cluster; u < p.units && ok; u += n_clusters) {
+      int m_blk, n_blk;
+      pair_tile(p, u, m_blk, n_blk);
+      const int m_row = m_blk * 256 + (int)rank * 128, n_row = n_blk * 256 + (int)rank * 64;
+      for (int kb = 0; kb < p.kblocks; ++kb) {
+        ok = __all_sync(0xffffffffu, wait8(done_bar(stage, 1), phase ^ 1, abort_flag, p.status));
+        if (!ok) break;
+        const uint32_t sa = smem_u32(smem + stage * PSTAGE_BYTES);
+        const uint32_t fb = cluster_addr(full_bar(stage), 0);
+        if (elected) {
           if (leader) mbar_expect_tx(full_bar(stage), 2 * PSTAGE_BYTES);
-          const uint32_t fb = cluster_addr(full_bar(stage), 0);
           tma_load_2d_pair(sa, &map_a, kb * BK, m_row, fb);
+          // this CTA's half of each column half: an MMA of N = 128 takes 64 rows of B from each CTA
           tma_load_2d_pair(sa + 128 * BK, &map_b, kb * BK, n_row, fb);
-          issued = min(issued + 1, S);
-          if (++stage == S) { stage = 0; phase ^= 1; }
+          tma_load_2d_pair(sa + 192 * BK, &map_b, kb * BK, n_row + 128, fb);
         }
+        __syncwarp();
+        issued = min(issued + 1, S);
+        if (++stage == S) { stage = 0; phase ^= 1; }
       }
-      // both CTAs' copies count on the leader's barriers: it sees them landed
-      // (bounded) before the final cluster barrier lets either CTA exit
-      if (leader)
-        for (int i = 0; i < issued; ++i) {
-          if (--stage < 0) { stage = S - 1; phase ^= 1; }
-          const uint64_t t0 = globaltimer();
-          while (!mbar_try(full_bar(stage), phase) && globaltimer() - t0 < kWaitNs) {}
-        }
     }
+    // both CTAs' copies count on the leader's barriers: it sees them landed
+    // (bounded) before the final cluster barrier lets either CTA exit
+    if (leader)
+      for (int i = 0; i < issued; ++i) {
+        if (--stage < 0) { stage = S - 1; phase ^= 1; }
+        const uint64_t t0 = globaltimer();
+        while (!mbar_try(full_bar(stage), phase) && globaltimer() - t0 < kWaitNs) {}
+      }
+    __syncwarp();
   } else if (warp == 1) {
     if (leader) {
       // ---------------- MMA issuer ----------------
-      // The warp stays converged and one elected lane issues, so descriptors
-      // are computed in uniform registers (measured below).
-      const uint32_t idesc = idesc8(256, 256);
+      const uint32_t idesc = idesc8(256, 128);
       const uint32_t elected = elect_one();
       const uint64_t desc0 = smem_desc(smem_u32(smem), 16, 1024);
       int stage = 0, acc = 0;
@@ -569,19 +619,24 @@ __global__ void __launch_bounds__(PTHREADS, 1)
       bool ok = true;
       for (int u = cluster; u < p.units && ok; u += n_clusters) {
         for (int kb = 0; kb < p.kblocks; ++kb) {
-          ok = mbar_wait(full_bar(stage), phase, abort_flag, p.status) &&
-               mbar_wait(tempty_bar(acc), acc_phase ^ 1, abort_flag, p.status);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          tc_fence_after();
-          const uint64_t ad = desc0 + (uint64_t)(stage * (PSTAGE_BYTES >> 4)), bd = ad + (128 * BK >> 4);
-          if (elected) {
+          ok = __all_sync(0xffffffffu, wait8(full_bar(stage), phase, abort_flag, p.status));
+          const uint64_t ad = desc0 + (uint64_t)(stage * (PSTAGE_BYTES >> 4));
 #pragma unroll
-            for (int kk = 0; kk < BK / 32; ++kk)
-              mma8_pair(tmem_base + acc * 256, ad + 2 * kk, bd + 2 * kk, idesc, kk > 0);
-            tc_commit_pair(done_bar(stage), 0x3);
+          for (int half = 0; half < 2; ++half) {
+            const int a = 2 * acc + half;
+            ok = ok && __all_sync(0xffffffffu, wait8(tempty_bar(a), acc_phase ^ 1, abort_flag, p.status));
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t bd = ad + ((128 + 64 * half) * BK >> 4);
+            if (elected) {
+#pragma unroll
+              for (int kk = 0; kk < BK / 32; ++kk)
+                mma8_pair(tmem_base + a * 128, ad + 2 * kk, bd + 2 * kk, idesc, kk > 0);
+              tc_commit_pair(done_bar(stage, half), 0x3);
+            }
+            __syncwarp();
           }
-          __syncwarp();
+          if (!ok) break;
           if (++stage == S) { stage = 0; phase ^= 1; }
           acc ^= 1;
           if (acc == 0) acc_phase ^= 1;
@@ -609,23 +664,32 @@ __global__ void __launch_bounds__(PTHREADS, 1)
     int acc = 0, stage = 0;
     uint32_t phase = 0;
     bool ok = true;
-    // This thread's two scales of K blocks kb and kb + 1, fetched two blocks
-    // ahead (a block takes less time than a load from L2).  Rows and columns
-    // outside the matrix take the scales of the last one inside; they are not stored.
-    constexpr int AHEAD = 2;
-    float fa[AHEAD], fb[AHEAD];
+    const uint32_t tempty0 = cluster_addr(tempty_bar(cg), 0);
+    // This thread's two scales of K blocks kb and kb + 1, fetched as one pair
+    // while the pair before is used (a wait for the older of two outstanding
+    // loads would be one for the newer too).  Rows and columns outside the
+    // matrix take the scales of the last one inside; they are not stored.
+    float fa[2], fb[2];
     const float *pa = nullptr, *pb = nullptr;
+    auto fetch = [&](int kb) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int k = min(kb + i, p.kblocks - 1);
+        fa[i] = pa[k * p.lsa];
+        fb[i] = pb[k];
+      }
+    };
     auto first_scales = [&](int u) {
       int m_blk, n_blk;
       pair_tile(p, u, m_blk, n_blk);
       pa = p.sa + min(m_blk * 256 + (int)rank * 128 + quarter * 32 + lane, p.M - 1);
       pb = p.sb + (int64_t)min(n_blk * 2 + cg, (p.N - 1) >> 7) * p.lsb;
-#pragma unroll
-      for (int i = 0; i < AHEAD; ++i) {
-        const int kb = min(i, p.kblocks - 1);
-        fa[i] = pa[kb * p.lsa];
-        fb[i] = pb[kb];
-      }
+      fetch(0);
+    };
+    auto wait_done = [&]() {
+      const bool r = __all_sync(0xffffffffu, wait8(done_bar(stage, cg), phase, abort_flag, p.status));
+      tc_fence_after();
+      return r;
     };
     if (cluster < p.units) first_scales(cluster);
     for (int u = cluster; u < p.units; u += n_clusters) {
@@ -635,7 +699,7 @@ __global__ void __launch_bounds__(PTHREADS, 1)
       const int n0 = n_blk * 256 + cg * 128;
       const bool mine = mw < p.M && n0 < p.N;
       const bool by_tma = n0 < p.n_tma, two = n0 + 64 < p.n_tma;
-      if (p.epi == EPI_ADD && mine && by_tma && lane == 0) {
+      if (EPI == EPI_ADD && mine && by_tma && lane == 0) {
         bulk_wait_read0();  // the previous tile's stores have read the boxes
         mbar_expect_tx(aux, two ? 2 * PBOX : PBOX);
         tma_load_2d(smem_u32(box), &map_d, n0, mw, aux);
@@ -645,50 +709,54 @@ __global__ void __launch_bounds__(PTHREADS, 1)
       uint64_t sum[64];
 #pragma unroll
       for (int i = 0; i < 64; ++i) sum[i] = 0;
-      for (int kb0 = 0; kb0 < p.kblocks && ok; kb0 += AHEAD) {
+      // Two 32-column loads are in flight while the two before are summed; the
+      // next K block's first two are requested before this block's last sums.
+      uint32_t v0[32], v1[32];
+      auto add = [&](uint32_t (&v)[32], int c, uint64_t f) {
 #pragma unroll
-        for (int i = 0; i < AHEAD; ++i) {
+        for (int j = 0; j < 16; ++j)
+          sum[16 * c + j] = fma2(f2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])), f, sum[16 * c + j]);
+      };
+      ok = wait_done();
+      if (ok) {
+        tmem_ld32_nw(t_row + acc * 256, v0);
+        tmem_ld32_nw(t_row + acc * 256 + 32, v1);
+      }
+      for (int kb0 = 0; kb0 < p.kblocks && ok; kb0 += 2) {
+        const float s2[2] = {fa[0] * fb[0], fa[1] * fb[1]};
+        if (kb0 + 2 < p.kblocks) fetch(kb0 + 2);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
           const int kb = kb0 + i;
           if (kb >= p.kblocks) break;
-          ok = __all_sync(0xffffffffu, mbar_wait(done_bar(stage), phase, abort_flag, p.status));
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t t = t_row + acc * 256;
-          uint32_t v[2][32];
-          tmem_ld32_nw(t, v[0]);
-          const float s = fa[i] * fb[i];
-          const uint64_t f = f2(s, s);
-          if (kb + AHEAD < p.kblocks) {
-            fa[i] = pa[(kb + AHEAD) * p.lsa];
-            fb[i] = pb[kb + AHEAD];
-          }
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            tmem_wait32(v[c & 1]);
-            if (c < 3) {
-              tmem_ld32_nw(t + 32 * (c + 1), v[(c + 1) & 1]);
-            } else {  // all read: the accumulator goes back before the last sums
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) {
-                if (leader) mbar_arrive(tempty_bar(acc));
-                else mbar_arrive_remote_relaxed(tempty_bar(acc), 0);
-              }
-            }
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-              sum[16 * c + j] = fma2(f2(__uint_as_float(v[c & 1][2 * j]), __uint_as_float(v[c & 1][2 * j + 1])), f,
-                                     sum[16 * c + j]);
-          }
+          const uint64_t f = f2(s2[i], s2[i]);
+          tmem_wait32(v0, v1);
+          add(v0, 0, f);
+          tmem_ld32_nw(t_row + acc * 256 + 64, v0);
+          add(v1, 1, f);
+          tmem_ld32_nw(t_row + acc * 256 + 96, v1);
+          tmem_wait32(v0, v1);
+          tc_fence_before();
+          __syncwarp();  // all lanes have read it: it goes back
+          if (lane == 0) mbar_arrive_relaxed(tempty0 + acc * 16);
           acc ^= 1;
           if (++stage == S) { stage = 0; phase ^= 1; }
+          add(v0, 2, f);
+          const bool more = kb + 1 < p.kblocks;
+          if (more) {
+            ok = wait_done();
+            if (!ok) break;
+            tmem_ld32_nw(t_row + acc * 256, v0);
+          }
+          add(v1, 3, f);
+          if (more) tmem_ld32_nw(t_row + acc * 256 + 32, v1);
         }
       }
       if (u + n_clusters < p.units) first_scales(u + n_clusters);
       if (!ok) break;
       if (!mine) continue;
-      if (p.epi == EPI_ADD && by_tma) {
-        ok = __all_sync(0xffffffffu, mbar_wait<true>(aux, aux_phase, abort_flag, p.status));
+      if (EPI == EPI_ADD && by_tma) {
+        ok = __all_sync(0xffffffffu, wait8(aux, aux_phase, abort_flag, p.status));
         if (!ok) break;
         aux_phase ^= 1;
         aux_inflight = false;
@@ -696,7 +764,7 @@ __global__ void __launch_bounds__(PTHREADS, 1)
         if (lane == 0) bulk_wait_read0();
         __syncwarp();
       }
-      if (p.epi == EPI_STORE_F32) {
+      if constexpr (EPI == EPI_STORE_F32) {
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
           if (b == 2) {
@@ -724,7 +792,7 @@ __global__ void __launch_bounds__(PTHREADS, 1)
         }
         continue;
       }
-      if (p.epi == EPI_RELU2_FP8) {
+      if constexpr (EPI == EPI_RELU2_FP8) {
         float a = 0.f;
 #pragma unroll
         for (int i = 0; i < 64; ++i) {
@@ -757,25 +825,25 @@ __global__ void __launch_bounds__(PTHREADS, 1)
         pair_tail<false, uint8_t>(p, my, lane, mw + lane, n0, 128);
         if (mw + lane < p.M) p.sd[(int64_t)(n0 >> 7) * p.lsd + mw + lane] = __fdiv_rn(a, fp8::kMax);
       } else {
-        if (p.epi == EPI_ADD) pair_tail<true, bf16>(p, my, lane, mw + lane, n0, 128);
+        if (EPI == EPI_ADD) pair_tail<true, bf16>(p, my, lane, mw + lane, n0, 128);
 #pragma unroll
         for (int q = 0; q < 16; ++q) {
           bf16 *d = reinterpret_cast<bf16 *>(my + (q >> 3) * PBOX + (((q & 7) ^ (lane & 7)) << 4));
           float o[8];
 #pragma unroll
           for (int j = 0; j < 4; ++j) f2split(sum[4 * q + j], o[2 * j], o[2 * j + 1]);
-          if (p.epi == EPI_ADD) {
+          if (EPI == EPI_ADD) {
             float old[8];
             Vec8<bf16>::load(d, old);
 #pragma unroll
             for (int j = 0; j < 8; ++j) o[j] += old[j];
-          } else if (p.epi == EPI_RELU2) {
+          } else if (EPI == EPI_RELU2) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
               o[j] = relu_nan(o[j]);
               o[j] *= o[j];
             }
-          } else if (p.epi == EPI_SOFTCAP) {
+          } else if (EPI == EPI_SOFTCAP) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) o[j] = softcap8(o[j]);
           }
@@ -787,7 +855,7 @@ __global__ void __launch_bounds__(PTHREADS, 1)
       __syncwarp();
       if (lane == 0) {
         if (by_tma) tma_store_2d(&map_d, smem_u32(box), n0, mw);
-        if (p.epi != EPI_RELU2_FP8 && two) tma_store_2d(&map_d, smem_u32(box) + PBOX, n0 + 64, mw);
+        if (EPI != EPI_RELU2_FP8 && two) tma_store_2d(&map_d, smem_u32(box) + PBOX, n0 + 64, mw);
         bulk_commit();
       }
     }
@@ -854,7 +922,7 @@ inline cudaError_t launch_rows(const GemmFp8Problem &g, int num_sms, int *status
 
 inline cudaError_t launch_pair(const GemmFp8Problem &g, int num_sms, int *status, cudaStream_t st) {
   CUtensorMap ma, mb, md;
-  bool ok = make_map8(&ma, g.A, g.M, g.K, g.lda, 128) && make_map8(&mb, g.B, g.N, g.K, g.ldb, 128);
+  bool ok = make_map8(&ma, g.A, g.M, g.K, g.lda, 128) && make_map8(&mb, g.B, g.N, g.K, g.ldb, 64);
   PairParams p;
   const int unit = g.epi == EPI_RELU2_FP8 ? 16 : g.epi == EPI_STORE_F32 ? 4 : 8;  // values in 16 bytes
   p.n_tma = g.N / unit * unit;
@@ -878,7 +946,7 @@ inline cudaError_t launch_pair(const GemmFp8Problem &g, int num_sms, int *status
   if ((int64_t)p.n_m * p.n_n > INT32_MAX / 2) return cudaErrorInvalidValue;  // unit + grid stays an int
   p.units = p.n_m * p.n_n;
   p.sa = g.sa; p.lsa = g.lsa; p.sb = g.sb; p.lsb = g.lsb; p.sd = g.sd; p.lsd = g.lsd;
-  p.epi = g.epi; p.status = status;
+  p.status = status;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * min(p.units, num_sms / 2));
   cfg.blockDim = dim3(PTHREADS);
@@ -891,7 +959,14 @@ inline cudaError_t launch_pair(const GemmFp8Problem &g, int num_sms, int *status
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, gemm_fp8_pair_kernel, ma, mb, md, p);
+  switch (g.epi) {
+    case EPI_STORE: return cudaLaunchKernelEx(&cfg, gemm_fp8_pair_kernel<EPI_STORE>, ma, mb, md, p);
+    case EPI_STORE_F32: return cudaLaunchKernelEx(&cfg, gemm_fp8_pair_kernel<EPI_STORE_F32>, ma, mb, md, p);
+    case EPI_ADD: return cudaLaunchKernelEx(&cfg, gemm_fp8_pair_kernel<EPI_ADD>, ma, mb, md, p);
+    case EPI_RELU2: return cudaLaunchKernelEx(&cfg, gemm_fp8_pair_kernel<EPI_RELU2>, ma, mb, md, p);
+    case EPI_SOFTCAP: return cudaLaunchKernelEx(&cfg, gemm_fp8_pair_kernel<EPI_SOFTCAP>, ma, mb, md, p);
+    default: return cudaLaunchKernelEx(&cfg, gemm_fp8_pair_kernel<EPI_RELU2_FP8>, ma, mb, md, p);
+  }
 }
 
 inline cudaError_t init() {
@@ -903,10 +978,18 @@ inline cudaError_t init() {
   big(gemm_fp8_rows_kernel<32>, RowsCfg<32>::kSmem);
   big(gemm_fp8_rows_kernel<64>, RowsCfg<64>::kSmem);
   big(gemm_fp8_rows_kernel<128>, RowsCfg<128>::kSmem);
-  big(gemm_fp8_pair_kernel, PSMEM);
-  cudaFuncAttributes a;
-  if (e == cudaSuccess) e = cudaFuncGetAttributes(&a, gemm_fp8_pair_kernel);
-  if (e == cudaSuccess && a.numRegs != PREGS) e = cudaErrorInvalidConfiguration;  // the register split would not add up
+  auto pair = [&](auto *k) {
+    big(k, PSMEM);
+    cudaFuncAttributes a;
+    if (e == cudaSuccess) e = cudaFuncGetAttributes(&a, k);
+    if (e == cudaSuccess && a.numRegs != PREGS) e = cudaErrorInvalidConfiguration;  // the register split would not add up
+  };
+  pair(gemm_fp8_pair_kernel<EPI_STORE>);
+  pair(gemm_fp8_pair_kernel<EPI_STORE_F32>);
+  pair(gemm_fp8_pair_kernel<EPI_ADD>);
+  pair(gemm_fp8_pair_kernel<EPI_RELU2>);
+  pair(gemm_fp8_pair_kernel<EPI_SOFTCAP>);
+  pair(gemm_fp8_pair_kernel<EPI_RELU2_FP8>);
   return e;
 }
 
