@@ -101,7 +101,33 @@ __device__ __forceinline__ float max16(float a) {
 // x' = x + res (rounded to T);  r = 1/sqrt(mean(x'^2) + eps);  y = r x' held in
 // e4m3 by blocks: since y / max|y| = x' / max|x'|, the codes come from x'
 // alone and only the scale, r max|x'| / 448, carries the norm.
-// One warp per row: the row is read once and stays in registers.
+// One warp per row: the row is read once and stays in registers, in its
+// storage type until it is used, so that all of its loads are in flight.
+template <typename T> struct Raw8;  // eight values as loaded
+template <> struct Raw8<bf16> {
+  uint4 u;
+  __device__ __forceinline__ void load(const bf16 *p) { u = __ldcs(reinterpret_cast<const uint4 *>(p)); }
+  __device__ __forceinline__ void get(float (&f)[8]) const {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      f[2 * j] = __uint_as_float(w[j] << 16);
+      f[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+    }
+  }
+};
+template <> struct Raw8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float *p) {
+    a = __ldcs(reinterpret_cast<const float4 *>(p));
+    b = __ldcs(reinterpret_cast<const float4 *>(p + 4));
+  }
+  __device__ __forceinline__ void get(float (&f)[8]) const {
+    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+  }
+};
+
 template <typename T, int NV, bool kRes>
 __global__ void __launch_bounds__(256) add_rmsnorm_fp8_kernel(const T *x, const T *res, T *x_out, uint8_t *__restrict__ q,
                                                               float *__restrict__ s, int64_t lds,
@@ -111,19 +137,29 @@ __global__ void __launch_bounds__(256) add_rmsnorm_fp8_kernel(const T *x, const 
   if (row >= M) return;
   const int nv = C >> 3;
   const size_t base = (size_t)row * C;
+  Raw8<T> xr[NV], rr[kRes ? NV : 1];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = lane + 32 * i;
+    if (c < nv) {
+      xr[i].load(x + base + c * 8);
+      if (kRes) rr[i].load(res + base + c * 8);
+    }
+  }
   float v[NV][8];
   float ss = 0.f;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int c = lane + 32 * i;
     if (c < nv) {
-      Vec8<T>::load(x + base + c * 8, v[i]);
+      xr[i].get(v[i]);
       if (kRes) {
         float w[8];
-        Vec8<T>::load(res + base + c * 8, w);
+        rr[i].get(w);
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[i][j] = to_f(from_f<T>(v[i][j] + w[j]));
       }
+      if (kRes || x_out != x) Vec8<T>::store(x_out + base + c * 8, v[i]);
 #pragma unroll
       for (int j = 0; j < 8; ++j) ss += v[i][j] * v[i][j];
     } else {
@@ -138,7 +174,6 @@ __global__ void __launch_bounds__(256) add_rmsnorm_fp8_kernel(const T *x, const 
     const int c = lane + 32 * i;
     const float a = max16(amax8(v[i]));
     if (c < nv) {
-      if (kRes || x_out != x) Vec8<T>::store(x_out + base + c * 8, v[i]);
       const Quant z(a);
       *reinterpret_cast<uint2 *>(q + base + c * 8) = quant8<T>(v[i], z);
       if ((lane & 15) == 0) s[(int64_t)(c >> 4) * lds + row] = __fdiv_rn(a * r, kMax);

@@ -141,40 +141,49 @@ template <int TN> struct RowsCfg {
                 "CTAs per SM");
 };
 
-struct RowsParams {
-  int M, N, kblocks;
-  int n_m, splits;      // CTAs per cluster
-  const float *sa, *sb;
-  int64_t lsa, lsb;
+// Where a product goes
+struct Out {
+  int M, N;
   void *D;
   int64_t ldd;
   float *sd;
   int64_t lsd;
+};
+
+struct RowsParams {
+  Out out;
+  int kblocks;
+  int n_m, splits;      // CTAs per cluster
+  const float *sa, *sb;
+  int64_t lsa, lsb;
   int epi;
   int *status;
 };
 
-// One activation row m, this lane's four weight rows [n, n + 4): v = sums
-__device__ __forceinline__ void rows_store(const RowsParams &p, int m, int n, float (&v)[4], int lane) {
+// Epilogue of a warp that holds one row m of a 128-column block, four columns
+// [n, n + 4) a lane: v = sums
+__device__ __forceinline__ void store_block_row(const Out &p, int epi, int m, int n, float (&v)[4], int lane) {
   const int left = p.N - n;  // <= 0: nothing to store (the lane still takes part in the block's maximum)
-  if (p.epi == EPI_STORE_F32) {
+  if (epi == EPI_STORE_F32) {
     float *d = reinterpret_cast<float *>(p.D) + (int64_t)m * p.ldd + n;
     if (left >= 4) *reinterpret_cast<float4 *>(d) = make_float4(v[0], v[1], v[2], v[3]);
     else
-      for (int j = 0; j < left; ++j) d[j] = v[j];
+#pragma unroll
+      for (int j = 0; j < 3; ++j)
+        if (j < left) d[j] = v[j];
     return;
   }
-  if (p.epi == EPI_RELU2 || p.epi == EPI_RELU2_FP8) {
+  if (epi == EPI_RELU2 || epi == EPI_RELU2_FP8) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       v[j] = relu_nan(v[j]);
       v[j] *= v[j];
     }
-  } else if (p.epi == EPI_SOFTCAP) {
+  } else if (epi == EPI_SOFTCAP) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) v[j] = softcap8(v[j]);
   }
-  if (p.epi == EPI_RELU2_FP8) {
+  if (epi == EPI_RELU2_FP8) {
     float a = 0.f;
 #pragma unroll
     for (int j = 0; j < 4; ++j)
@@ -186,13 +195,15 @@ __device__ __forceinline__ void rows_store(const RowsParams &p, int m, int n, fl
     uint8_t *d = reinterpret_cast<uint8_t *>(p.D) + (int64_t)m * p.ldd + n;
     if (left >= 4) *reinterpret_cast<uint32_t *>(d) = c;
     else
-      for (int j = 0; j < left; ++j) d[j] = (uint8_t)(c >> (8 * j));
+#pragma unroll
+      for (int j = 0; j < 3; ++j)
+        if (j < left) d[j] = (uint8_t)(c >> (8 * j));
     if (lane == 0) p.sd[(int64_t)(n >> 7) * p.lsd + m] = __fdiv_rn(a, fp8::kMax);
     return;
   }
   bf16 *d = reinterpret_cast<bf16 *>(p.D) + (int64_t)m * p.ldd + n;
   if (left >= 4) {
-    if (p.epi == EPI_ADD) {
+    if (epi == EPI_ADD) {
       float old[4];
       Vec4<bf16>::load(d, old);
 #pragma unroll
@@ -200,13 +211,22 @@ __device__ __forceinline__ void rows_store(const RowsParams &p, int m, int n, fl
     }
     Vec4<bf16>::store(d, v);
   } else {
-    for (int j = 0; j < left; ++j)
-      d[j] = __float2bfloat16_rn(p.epi == EPI_ADD ? __bfloat162float(d[j]) + v[j] : v[j]);
+#pragma unroll
+    for (int j = 0; j < 3; ++j)
+      if (j < left) d[j] = __float2bfloat16_rn(epi == EPI_ADD ? __bfloat162float(d[j]) + v[j] : v[j]);
   }
 }
 
 __device__ __forceinline__ void cluster_started(int splits) {
   if (splits > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float4 ld_cluster(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
 }
 __device__ __forceinline__ void st_cluster(uint32_t addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
@@ -345,7 +365,7 @@ __global__ void __launch_bounds__(RowsCfg<TN>::kThreads, RowsCfg<TN>::kCtas)
 #pragma unroll
       for (int i = 0; i < NS; ++i) {
         const int c = lane + 32 * i, m = m0 + c0 + c;
-        fa[i] = (c < COLS && m < p.M) ? p.sa[(int64_t)kb * p.lsa + m] : 0.f;
+        fa[i] = (c < COLS && m < p.out.M) ? p.sa[(int64_t)kb * p.lsa + m] : 0.f;
       }
     };
     if (kb0 < kb1) fetch(kb0);
@@ -389,7 +409,7 @@ __global__ void __launch_bounds__(RowsCfg<TN>::kThreads, RowsCfg<TN>::kCtas)
 #pragma unroll
     for (int i = 0; i < COLS; ++i) {
       const int c = c0 + i;
-      if (m0 + c < p.M) {
+      if (m0 + c < p.out.M) {
         float lo, hi;
         f2split(sum[i / 2], lo, hi);
         st_cluster(cluster_addr(to + (c & (per - 1)) * 512, c >> shift), (i & 1) ? hi : lo);
@@ -403,7 +423,7 @@ __global__ void __launch_bounds__(RowsCfg<TN>::kThreads, RowsCfg<TN>::kCtas)
   if (warp == 1) tmem_dealloc(tmem_base, Cfg::kTmemCols);
   // one warp per activation row: 128 weight rows are one 1 x 128 output block
   const int per = TN / p.splits;
-  for (int c = warp; c < per && m0 + rank * per + c < p.M; c += Cfg::kThreads / 32) {
+  for (int c = warp; c < per && m0 + rank * per + c < p.out.M; c += Cfg::kThreads / 32) {
     const float *at = sums + c * 128 + lane * 4;
     float v[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
@@ -411,7 +431,7 @@ __global__ void __launch_bounds__(RowsCfg<TN>::kThreads, RowsCfg<TN>::kCtas)
       const float4 f = *reinterpret_cast<const float4 *>(at + r * per * 128);
       v[0] += f.x; v[1] += f.y; v[2] += f.z; v[3] += f.w;
     }
-    rows_store(p, m0 + rank * per + c, n0 + lane * 4, v, lane);
+    store_block_row(p.out, p.epi, m0 + rank * per + c, n0 + lane * 4, v, lane);
   }
 }
 
@@ -428,6 +448,10 @@ __global__ void __launch_bounds__(RowsCfg<TN>::kThreads, RowsCfg<TN>::kCtas)
 // A thread's 128 columns are also one 1 x 128 output block, so the 8-bit
 // epilogue finds its maximum without leaving the thread.
 //
+// Few tiles leave SMs idle, so K is cut over the pairs of a larger cluster (2
+// or 4): each CTA then leaves its sums in its ring's memory and adds, for its
+// part of the rows, those of the cluster's pairs in order.
+//
 // Each epilogue warp stages its 32 rows x 128 columns alone, in two boxes of
 // 32 rows x 128 bytes (128-byte swizzle) that leave by TMA; an epilogue that
 // adds to D has them loaded while the K loop runs.
@@ -441,22 +465,21 @@ constexpr int PEPI_WARPS = 8;
 constexpr int PTHREADS = 128 + 32 * PEPI_WARPS;
 constexpr int PREGS = 168, PREGS_LOW = 24, PREGS_HIGH = 240;
 static_assert(128 * PREGS_LOW + 32 * PEPI_WARPS * PREGS_HIGH <= PTHREADS * PREGS, "register split within the launch");
+constexpr int PSPLITS = 4;  // pairs per cluster at most: eight CTAs
 constexpr int PBOX = 32 * 128;
 constexpr int PSMEM = PSTAGES * PSTAGE_BYTES + PEPI_WARPS * 2 * PBOX + 256 + 1024;
 static_assert(PSMEM <= 232448, "shared memory per CTA");
+static_assert(128 * 256 * 4 <= PSTAGES * PSTAGE_BYTES, "a split's sums fit the ring");
 
 // A TMA store writes whole 16-byte units of a row (measured: one byte per
 // element, N % 16 == 8, wrote eight bytes past N), so the map of D ends at the
 // last whole unit, column n_tma, and the threads take the rest of their row.
 struct PairParams {
-  int M, N, kblocks;
+  Out out;
+  int kblocks, splits;  // pairs per cluster
   int n_m, n_n, units, n_tma;
-  void *D;
-  int64_t ldd;
   const float *sa, *sb;
   int64_t lsa, lsb;
-  float *sd;
-  int64_t lsd;
   int *status;
 };
 
@@ -464,11 +487,11 @@ struct PairParams {
 // warp's staged boxes (row at `my`, column n at byte 0), es bytes each.
 template <bool kLoad, typename E>
 __device__ __forceinline__ void pair_tail(const PairParams &p, uint8_t *my, int lane, int m, int n, int width) {
-  if (m >= p.M) return;
-  for (int c = max(p.n_tma, n); c < min(p.N, n + width); ++c) {
+  if (m >= p.out.M) return;
+  for (int c = max(p.n_tma, n); c < min(p.out.N, n + width); ++c) {
     const int b = (c - n) * (int)sizeof(E);
     E *e = reinterpret_cast<E *>(my + (b >> 7) * PBOX + ((((b >> 4) & 7) ^ (lane & 7)) << 4) + (b & 15));
-    E *d = reinterpret_cast<E *>(p.D) + (int64_t)m * p.ldd + c;
+    E *d = reinterpret_cast<E *>(p.out.D) + (int64_t)m * p.out.ldd + c;
     if (kLoad) *e = *d;
     else *d = *e;
   }
@@ -533,9 +556,14 @@ __global__ void __launch_bounds__(PTHREADS, 1)
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   static_assert((3 * S + 5 + PEPI_WARPS) * 8 + 8 <= 256, "barriers, TMEM slot and abort flag fit their 256 bytes");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_rank();
+  // a cluster holds `splits` pairs; each takes its part of K of the same tile
+  const uint32_t cta = cluster_rank(), lead = cta & ~1u, rank = cta & 1;
   const bool leader = rank == 0;
-  const int cluster = blockIdx.x >> 1, n_clusters = gridDim.x >> 1;
+  const uint16_t both = (uint16_t)(0x3 << lead);
+  const int cluster = blockIdx.x / (2 * p.splits), n_clusters = gridDim.x / (2 * p.splits);
+  const int split = (int)(cta >> 1);
+  const int kb0 = (int)((int64_t)p.kblocks * split / p.splits);
+  const int kb1 = (int)((int64_t)p.kblocks * (split + 1) / p.splits);
   auto full_bar = [&](int s) { return smem_u32(bars + s); };
   // done[s, h]: the MMAs of stage s and column half h are complete, so that
   // half of its accumulator is full, and with h = 1, the second, the stage is free.
@@ -582,11 +610,11 @@ __global__ void __launch_bounds__(PTHREADS, 1)
       int m_blk, n_blk;
       pair_tile(p, u, m_blk, n_blk);
       const int m_row = m_blk * 256 + (int)rank * 128, n_row = n_blk * 256 + (int)rank * 64;
-      for (int kb = 0; kb < p.kblocks; ++kb) {
+      for (int kb = kb0; kb < kb1; ++kb) {
         ok = __all_sync(0xffffffffu, wait8(done_bar(stage, 1), phase ^ 1, abort_flag, p.status));
         if (!ok) break;
         const uint32_t sa = smem_u32(smem + stage * PSTAGE_BYTES);
-        const uint32_t fb = cluster_addr(full_bar(stage), 0);
+        const uint32_t fb = cluster_addr(full_bar(stage), lead);
         if (elected) {
           if (leader) mbar_expect_tx(full_bar(stage), 2 * PSTAGE_BYTES);
           tma_load_2d_pair(sa, &map_a, kb * BK, m_row, fb);
@@ -600,7 +628,7 @@ __global__ void __launch_bounds__(PTHREADS, 1)
       }
     }
     // both CTAs' copies count on the leader's barriers: it sees them landed
-    // (bounded) before the final cluster barrier lets either CTA exit
+    // (bounded) before the next cluster barrier
     if (leader)
       for (int i = 0; i < issued; ++i) {
         if (--stage < 0) { stage = S - 1; phase ^= 1; }
@@ -618,7 +646,7 @@ __global__ void __launch_bounds__(PTHREADS, 1)
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
       for (int u = cluster; u < p.units && ok; u += n_clusters) {
-        for (int kb = 0; kb < p.kblocks; ++kb) {
+        for (int kb = kb0; kb < kb1; ++kb) {
           ok = __all_sync(0xffffffffu, wait8(full_bar(stage), phase, abort_flag, p.status));
           const uint64_t ad = desc0 + (uint64_t)(stage * (PSTAGE_BYTES >> 4));
 #pragma unroll
@@ -632,7 +660,7 @@ __global__ void __launch_bounds__(PTHREADS, 1)
 #pragma unroll
               for (int kk = 0; kk < BK / 32; ++kk)
                 mma8_pair(tmem_base + a * 128, ad + 2 * kk, bd + 2 * kk, idesc, kk > 0);
-              tc_commit_pair(done_bar(stage, half), 0x3);
+              tc_commit_pair(done_bar(stage, half), both);
             }
             __syncwarp();
           }
@@ -643,13 +671,14 @@ __global__ void __launch_bounds__(PTHREADS, 1)
         }
       }
       if (elected) {
-        tc_commit_pair(drain_bar, 0x1);
+        tc_commit_pair(drain_bar, (uint16_t)(1 << lead));
         const uint64_t t0 = globaltimer();
         while (!mbar_try(drain_bar, 0) && globaltimer() - t0 < kWaitNs) {}
       }
       __syncwarp();
     }
   }
+  if (p.splits > 1) cluster_sync_all();  // the split sums (below)
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(PREGS_HIGH));
     // ---------------- epilogue warps 4..11 (both CTAs) ----------------
@@ -664,7 +693,7 @@ __global__ void __launch_bounds__(PTHREADS, 1)
     int acc = 0, stage = 0;
     uint32_t phase = 0;
     bool ok = true;
-    const uint32_t tempty0 = cluster_addr(tempty_bar(cg), 0);
+    const uint32_t tempty0 = cluster_addr(tempty_bar(cg), lead);
     // This thread's two scales of K blocks kb and kb + 1, fetched as one pair
     // while the pair before is used (a wait for the older of two outstanding
     // loads would be one for the newer too).  Rows and columns outside the
@@ -674,7 +703,7 @@ __global__ void __launch_bounds__(PTHREADS, 1)
     auto fetch = [&](int kb) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int k = min(kb + i, p.kblocks - 1);
+        const int k = min(kb + i, kb1 - 1);
         fa[i] = pa[k * p.lsa];
         fb[i] = pb[k];
       }
@@ -682,9 +711,9 @@ __global__ void __launch_bounds__(PTHREADS, 1)
     auto first_scales = [&](int u) {
       int m_blk, n_blk;
       pair_tile(p, u, m_blk, n_blk);
-      pa = p.sa + min(m_blk * 256 + (int)rank * 128 + quarter * 32 + lane, p.M - 1);
-      pb = p.sb + (int64_t)min(n_blk * 2 + cg, (p.N - 1) >> 7) * p.lsb;
-      fetch(0);
+      pa = p.sa + min(m_blk * 256 + (int)rank * 128 + quarter * 32 + lane, p.out.M - 1);
+      pb = p.sb + (int64_t)min(n_blk * 2 + cg, (p.out.N - 1) >> 7) * p.lsb;
+      fetch(kb0);
     };
     auto wait_done = [&]() {
       const bool r = __all_sync(0xffffffffu, wait8(done_bar(stage, cg), phase, abort_flag, p.status));
@@ -697,9 +726,9 @@ __global__ void __launch_bounds__(PTHREADS, 1)
       pair_tile(p, u, m_blk, n_blk);
       const int mw = m_blk * 256 + (int)rank * 128 + quarter * 32;  // this warp's first row
       const int n0 = n_blk * 256 + cg * 128;
-      const bool mine = mw < p.M && n0 < p.N;
+      const bool mine = mw < p.out.M && n0 < p.out.N;
       const bool by_tma = n0 < p.n_tma, two = n0 + 64 < p.n_tma;
-      if (EPI == EPI_ADD && mine && by_tma && lane == 0) {
+      if (EPI == EPI_ADD && p.splits == 1 && mine && by_tma && lane == 0) {
         bulk_wait_read0();  // the previous tile's stores have read the boxes
         mbar_expect_tx(aux, two ? 2 * PBOX : PBOX);
         tma_load_2d(smem_u32(box), &map_d, n0, mw, aux);
@@ -722,13 +751,13 @@ __global__ void __launch_bounds__(PTHREADS, 1)
         tmem_ld32_nw(t_row + acc * 256, v0);
         tmem_ld32_nw(t_row + acc * 256 + 32, v1);
       }
-      for (int kb0 = 0; kb0 < p.kblocks && ok; kb0 += 2) {
+      for (int kp = kb0; kp < kb1 && ok; kp += 2) {
         const float s2[2] = {fa[0] * fb[0], fa[1] * fb[1]};
-        if (kb0 + 2 < p.kblocks) fetch(kb0 + 2);
+        if (kp + 2 < kb1) fetch(kp + 2);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const int kb = kb0 + i;
-          if (kb >= p.kblocks) break;
+          const int kb = kp + i;
+          if (kb >= kb1) break;
           const uint64_t f = f2(s2[i], s2[i]);
           tmem_wait32(v0, v1);
           add(v0, 0, f);
@@ -742,7 +771,7 @@ __global__ void __launch_bounds__(PTHREADS, 1)
           acc ^= 1;
           if (++stage == S) { stage = 0; phase ^= 1; }
           add(v0, 2, f);
-          const bool more = kb + 1 < p.kblocks;
+          const bool more = kb + 1 < kb1;
           if (more) {
             ok = wait_done();
             if (!ok) break;
@@ -754,6 +783,22 @@ __global__ void __launch_bounds__(PTHREADS, 1)
       }
       if (u + n_clusters < p.units) first_scales(u + n_clusters);
       if (!ok) break;
+      if (p.splits > 1) {  // the cluster's only tile: its sums go to shared memory
+        const int last = stage ? stage - 1 : S - 1;
+        ok = __all_sync(0xffffffffu, wait8(done_bar(last, 1), stage ? phase : phase ^ 1, abort_flag, p.status));
+        if (!ok) break;
+        // no MMA reads the ring and no copy is on its way to it any more
+        const int row = quarter * 32 + lane;
+        uint8_t *const to = smem + row * 1024;  // 16-byte unit u of a row sits at u ^ (row % 8)
+#pragma unroll
+        for (int q = 0; q < 32; ++q) {
+          float o[4];
+          f2split(sum[2 * q], o[0], o[1]);
+          f2split(sum[2 * q + 1], o[2], o[3]);
+          *reinterpret_cast<float4 *>(to + (((cg * 32 + q) ^ (row & 7)) << 4)) = make_float4(o[0], o[1], o[2], o[3]);
+        }
+        break;
+      }
       if (!mine) continue;
       if (EPI == EPI_ADD && by_tma) {
         ok = __all_sync(0xffffffffu, wait8(aux, aux_phase, abort_flag, p.status));
@@ -823,7 +868,7 @@ __global__ void __launch_bounds__(PTHREADS, 1)
           *reinterpret_cast<uint4 *>(my + ((q ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
         }
         pair_tail<false, uint8_t>(p, my, lane, mw + lane, n0, 128);
-        if (mw + lane < p.M) p.sd[(int64_t)(n0 >> 7) * p.lsd + mw + lane] = __fdiv_rn(a, fp8::kMax);
+        if (mw + lane < p.out.M) p.out.sd[(int64_t)(n0 >> 7) * p.out.lsd + mw + lane] = __fdiv_rn(a, fp8::kMax);
       } else {
         if (EPI == EPI_ADD) pair_tail<true, bf16>(p, my, lane, mw + lane, n0, 128);
 #pragma unroll
@@ -859,6 +904,35 @@ __global__ void __launch_bounds__(PTHREADS, 1)
         bulk_commit();
       }
     }
+    if (p.splits > 1) {
+      cluster_sync_all();  // every pair's sums are in shared memory
+      // This CTA's part of its rows: one warp per row and 128-column block, the
+      // pairs' sums added in order, four such rows' reads in flight.
+      int m_blk, n_blk;
+      pair_tile(p, cluster, m_blk, n_blk);
+      const int per = 128 / p.splits, first = m_blk * 256 + (int)rank * 128;
+#pragma unroll 1
+      for (int i0 = (warp - 4) * 4; i0 < 2 * per && ok; i0 += 4 * PEPI_WARPS) {
+        float4 f[4][PSPLITS];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int row = split * per + ((i0 + q) >> 1), unit = ((i0 + q) & 1) * 32 + lane;
+          const uint32_t at = smem_u32(smem) + row * 1024 + ((unit ^ (row & 7)) << 4);
+#pragma unroll
+          for (int r = 0; r < PSPLITS; ++r)
+            if (r < p.splits) f[q][r] = ld_cluster(cluster_addr(at, 2 * r + rank));
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int m = first + split * per + ((i0 + q) >> 1), n = n_blk * 256 + ((i0 + q) & 1) * 128;
+          float v[4] = {f[q][0].x, f[q][0].y, f[q][0].z, f[q][0].w};
+#pragma unroll
+          for (int r = 1; r < PSPLITS; ++r)
+            if (r < p.splits) { v[0] += f[q][r].x; v[1] += f[q][r].y; v[2] += f[q][r].z; v[3] += f[q][r].w; }
+          if (m < p.out.M && n < p.out.N) store_block_row(p.out, EPI, m, n + lane * 4, v, lane);
+        }
+      }
+    }
     if (lane == 0) {
       bulk_wait0();
       // only after an abort: a load of D that was never taken lands first (bounded)
@@ -890,16 +964,19 @@ inline bool make_map8(CUtensorMap *map, const void *base, int64_t rows, int64_t 
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+inline Out out_of(const GemmFp8Problem &g) { return Out{g.M, g.N, g.D, g.ldd, g.sd, g.lsd}; }
+
 template <int TN>
 inline cudaError_t launch_rows(const GemmFp8Problem &g, int num_sms, int *status, cudaStream_t st) {
   using Cfg = RowsCfg<TN>;
   CUtensorMap mw, mx;
   if (!make_map8(&mw, g.B, g.N, g.K, g.ldb, 128) || !make_map8(&mx, g.A, g.M, g.K, g.lda, TN)) return cudaErrorInvalidValue;
   RowsParams p;
-  p.M = g.M; p.N = g.N; p.kblocks = (g.K + BK - 1) / BK;
+  p.out = out_of(g);
+  p.kblocks = (g.K + BK - 1) / BK;
   p.n_m = (g.M + TN - 1) / TN;
   p.sa = g.sa; p.lsa = g.lsa; p.sb = g.sb; p.lsb = g.lsb;
-  p.D = g.D; p.ldd = g.ldd; p.sd = g.sd; p.lsd = g.lsd; p.epi = g.epi; p.status = status;
+  p.epi = g.epi; p.status = status;
   const int64_t tiles = (int64_t)p.n_m * ((g.N + 127) / 128);
   // cut K while every CTA still finds a place at once and keeps a K block
   p.splits = 1;
@@ -939,22 +1016,28 @@ inline cudaError_t launch_pair(const GemmFp8Problem &g, int num_sms, int *status
     ok = ok && make_map(&md, g.D, g.M, cols, g.ldd, 64, 32);
   }
   if (!ok) return cudaErrorInvalidValue;
-  p.D = g.D; p.ldd = g.ldd;
-  p.M = g.M; p.N = g.N; p.kblocks = (g.K + BK - 1) / BK;
+  p.out = out_of(g);
+  p.kblocks = (g.K + BK - 1) / BK;
   p.n_m = (g.M + 255) / 256;
   p.n_n = (g.N + 255) / 256;
   if ((int64_t)p.n_m * p.n_n > INT32_MAX / 2) return cudaErrorInvalidValue;  // unit + grid stays an int
   p.units = p.n_m * p.n_n;
-  p.sa = g.sa; p.lsa = g.lsa; p.sb = g.sb; p.lsb = g.lsb; p.sd = g.sd; p.lsd = g.lsd;
+  p.sa = g.sa; p.lsa = g.lsa; p.sb = g.sb; p.lsb = g.lsb;
   p.status = status;
+  p.splits = 1;
+  // A split costs about 6 us to exchange its sums (15 bytes a cycle and SM
+  // between shared memories), what ten K blocks take; with twelve blocks left
+  // to each it pays (512 x 1536 x 6144: 31.1 us whole, 19.6 us in four; 1024 x
+  // 1280 x 1280: 12.0 us whole, 14.9 us in two).
+  while (p.splits < PSPLITS && p.kblocks >= 24 * p.splits && p.units * 2 * p.splits <= num_sms / 2) p.splits *= 2;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * min(p.units, num_sms / 2));
+  cfg.gridDim = dim3(2 * p.splits * min(p.units, num_sms / 2));
   cfg.blockDim = dim3(PTHREADS);
   cfg.dynamicSmemBytes = PSMEM;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.x = 2 * p.splits;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
