@@ -9,8 +9,8 @@
 // Which code a value gets is decided exactly for bf16 inputs: z = 448 v / a is
 // the quotient of integers below 2^11 and 2^8 times a power of two, so it is
 // either a rounding border of e4m3 (at most 5 significant bits) or at least
-// 2^-13 away from every one, relatively.  v * RN(448 / a) is within 2^-23 of
-// z, so rounding it to 16 significant bits first puts every border case back
+// 2^-13 away from every one, relatively.  v times an approximate 448 / a is
+// within 2^-20 of z, so rounding it to 16 significant bits first puts every border case back
 // on the border and moves no other value across one: the result is the
 // round-to-nearest-even of the exact quotient, without a division per value.
 // fp32 inputs take RN(RN(448 v) / a), one IEEE division per value.
@@ -35,14 +35,17 @@ __device__ __forceinline__ uint32_t cvt4(float a, float b, float c, float d) {
 }
 
 // What turns a block's values into codes, from the block's largest magnitude
-// a.  Blocks below 2^-100 are scaled up by 2^100 first (exact), because
+// a: the factor 448 / a to 2^-21 (the approximate reciprocal is within one
+// unit).  Blocks below 2^-100 are scaled up by 2^100 first (exact), because
 // 448 / a would overflow.
 struct Quant {
   float a, inv, pre;
   __device__ __forceinline__ explicit Quant(float amax) {
     pre = amax < 0x1p-100f ? 0x1p100f : 1.f;
     a = amax * pre;
-    inv = a > 0.f ? __fdiv_rn(kMax, a) : 0.f;
+    float r;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(a));
+    inv = a > 0.f ? kMax * r : 0.f;
   }
 };
 
@@ -58,30 +61,41 @@ __device__ __forceinline__ uint64_t round16(uint64_t y) {
 template <typename T> __device__ __forceinline__ uint2 quant8(const float (&v)[8], const Quant &z);
 template <> __device__ __forceinline__ uint2 quant8<bf16>(const float (&v)[8], const Quant &z) {
   const uint64_t f = f2(z.inv, z.inv), p = f2(z.pre, z.pre);
-  uint32_t h[4];
+  float y[8];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const uint64_t y = round16(mul2(mul2(f2(v[2 * j], v[2 * j + 1]), p), f));
-    float lo, hi;
-    f2split(y, lo, hi);
-    h[j] = cvt2(lo, hi);
+    uint64_t w = f2(v[2 * j], v[2 * j + 1]);
+    if (z.pre != 1.f) w = mul2(w, p);
+    f2split(round16(mul2(w, f)), y[2 * j], y[2 * j + 1]);
   }
-  return make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+  return make_uint2(cvt4(y[0], y[1], y[2], y[3]), cvt4(y[4], y[5], y[6], y[7]));
 }
 template <> __device__ __forceinline__ uint2 quant8<float>(const float (&v)[8], const Quant &z) {
-  uint32_t h[4];
-  // above 2^100 the product 448 v could overflow: scaled down instead (exact)
-  const float pre = z.a > 0x1p100f ? 0x1p-100f : z.pre;
-  const float a = z.a > 0x1p100f ? z.a * 0x1p-100f : z.a;
+  // v times the approximate 448 / a is within 2^-20 of RN(RN(448 v) / a).  Only
+  // where it lies that close to a value of six significant bits, which every
+  // border is, can the two get different codes: those (one value in 2^14) take
+  // the division.
+  const uint64_t f = f2(z.inv, z.inv), p = f2(z.pre, z.pre), k = f2(262145.f, 262145.f), m1 = f2(-1.f, -1.f);
+  float y[8];
+  bool near = false;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    float y[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      y[i] = a != 0.f ? __fdiv_rn(__fmul_rn(v[2 * j + i] * pre, kMax), a) : v[2 * j + i];  // 0 or NaN
-    h[j] = cvt2(y[0], y[1]);
+    const uint64_t q = mul2(mul2(f2(v[2 * j], v[2 * j + 1]), p), f);
+    const uint64_t t = mul2(q, k);
+    const uint64_t h = fma2(fma2(q, m1, t), m1, t);  // q to six bits
+    float e0, e1;
+    f2split(fma2(h, m1, q), e0, e1);
+    f2split(q, y[2 * j], y[2 * j + 1]);
+    near |= fabsf(e0) < fabsf(y[2 * j]) * 0x1p-20f || fabsf(e1) < fabsf(y[2 * j + 1]) * 0x1p-20f;  // not for 0
   }
-  return make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+  if (near && z.a > 0.f) {
+    // above 2^100 the product 448 v could overflow: scaled down instead (exact)
+    const float pre = z.a > 0x1p100f ? 0x1p-100f : z.pre;
+    const float a = z.a > 0x1p100f ? z.a * 0x1p-100f : z.a;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) y[j] = __fdiv_rn(__fmul_rn(v[j] * pre, kMax), a);
+  }
+  return make_uint2(cvt4(y[0], y[1], y[2], y[3]), cvt4(y[4], y[5], y[6], y[7]));
 }
 
 __device__ __forceinline__ float amax8(const float (&v)[8]) {
@@ -101,12 +115,18 @@ __device__ __forceinline__ float max16(float a) {
 // x' = x + res (rounded to T);  r = 1/sqrt(mean(x'^2) + eps);  y = r x' held in
 // e4m3 by blocks: since y / max|y| = x' / max|x'|, the codes come from x'
 // alone and only the scale, r max|x'| / 448, carries the norm.
-// One warp per row: the row is read once and stays in registers, in its
-// storage type until it is used, so that all of its loads are in flight.
+// WPR warps per row (one where there are rows enough to fill the SMs, four
+// otherwise): the row is read once and stays in registers, in its storage type
+// until it is used, so that all of its loads are in flight.
 template <typename T> struct Raw8;  // eight values as loaded
 template <> struct Raw8<bf16> {
   uint4 u;
   __device__ __forceinline__ void load(const bf16 *p) { u = __ldcs(reinterpret_cast<const uint4 *>(p)); }
+  __device__ __forceinline__ float amax() const {  // largest magnitude, two at a time
+    const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&u);
+    const __nv_bfloat162 m = __hmax2(__hmax2(__habs2(h[0]), __habs2(h[1])), __hmax2(__habs2(h[2]), __habs2(h[3])));
+    return fmaxf(__low2float(m), __high2float(m));
+  }
   __device__ __forceinline__ void get(float (&f)[8]) const {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
@@ -122,26 +142,32 @@ template <> struct Raw8<float> {
     a = __ldcs(reinterpret_cast<const float4 *>(p));
     b = __ldcs(reinterpret_cast<const float4 *>(p + 4));
   }
+  __device__ __forceinline__ float amax() const {
+    return fmaxf(fmaxf(fmaxf(fabsf(a.x), fabsf(a.y)), fmaxf(fabsf(a.z), fabsf(a.w))),
+                 fmaxf(fmaxf(fabsf(b.x), fabsf(b.y)), fmaxf(fabsf(b.z), fabsf(b.w))));
+  }
   __device__ __forceinline__ void get(float (&f)[8]) const {
     f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
     f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
   }
 };
 
-template <typename T, int NV, bool kRes>
+template <typename T, int NV, int WPR, bool kRes>
 __global__ void __launch_bounds__(256) add_rmsnorm_fp8_kernel(const T *x, const T *res, T *x_out, uint8_t *__restrict__ q,
                                                               float *__restrict__ s, int64_t lds,
                                                               float *__restrict__ r_out, int M, int C) {
-  const int row = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (row >= M) return;
+  constexpr int T_ROW = 32 * WPR;  // threads per row
+  const int row = blockIdx.x * (256 / T_ROW) + threadIdx.x / T_ROW;
+  const int lane = threadIdx.x % T_ROW;
+  if (WPR == 1 && row >= M) return;  // with more, whole warps of a missing row take part in the barrier
+  const bool in = row < M;
   const int nv = C >> 3;
   const size_t base = (size_t)row * C;
   Raw8<T> xr[NV], rr[kRes ? NV : 1];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int c = lane + 32 * i;
-    if (c < nv) {
+    const int c = lane + T_ROW * i;
+    if (in && c < nv) {
       xr[i].load(x + base + c * 8);
       if (kRes) rr[i].load(res + base + c * 8);
     }
@@ -150,8 +176,8 @@ __global__ void __launch_bounds__(256) add_rmsnorm_fp8_kernel(const T *x, const 
   float ss = 0.f;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int c = lane + 32 * i;
-    if (c < nv) {
+    const int c = lane + T_ROW * i;
+    if (in && c < nv) {
       xr[i].get(v[i]);
       if (kRes) {
         float w[8];
@@ -168,91 +194,145 @@ __global__ void __launch_bounds__(256) add_rmsnorm_fp8_kernel(const T *x, const 
     }
   }
   ss = warp_sum(ss);
+  if constexpr (WPR > 1) {
+    __shared__ float part[8];
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = ss;
+    __syncthreads();
+    const int w0 = threadIdx.x / T_ROW * WPR;
+    ss = 0.f;
+#pragma unroll
+    for (int w = 0; w < WPR; ++w) ss += part[w0 + w];
+  }
   const float r = rsqrtf(ss / (float)C + kEps);
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int c = lane + 32 * i;
+    const int c = lane + T_ROW * i;
     const float a = max16(amax8(v[i]));
-    if (c < nv) {
+    if (in && c < nv) {
       const Quant z(a);
       *reinterpret_cast<uint2 *>(q + base + c * 8) = quant8<T>(v[i], z);
       if ((lane & 15) == 0) s[(int64_t)(c >> 4) * lds + row] = __fdiv_rn(a * r, kMax);
     }
   }
-  if (r_out && lane == 0) r_out[row] = r;
+  if (r_out && in && lane == 0) r_out[row] = r;
 }
 
 // ---------------------------------------------------------------------------
-// 1 x 128 blocks: a warp takes 256 columns of one row, 16 lanes to a block.
+// 1 x 128 blocks: a warp takes 256 columns of four rows, 16 lanes to a block,
+// a CTA 32 rows of the same columns.  Lanes 0..3 and 16..19 then hold one
+// row's maximum each, so the four rows' scales take one division and one store.
+// (Measured against CTAs that walk several units with the next one's loads in
+// flight: 23.9 against 26.8 us at 16,384 x 2048 bf16.)
 template <typename T>
 __global__ void __launch_bounds__(256) quant_rows_kernel(const T *__restrict__ x, int64_t ldx, uint8_t *__restrict__ q,
                                                          int64_t ldq, float *__restrict__ s, int64_t lds, int rows,
-                                                         int cols) {
+                                                         int cols, unsigned segs) {
   const int lane = threadIdx.x & 31;
-  const int segs = (cols + 255) >> 8;
-  const int64_t unit = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-  const int64_t row = unit / segs;
-  if (row >= rows) return;
-  const int col = (int)(unit % segs) * 256 + lane * 8;
-  float v[8] = {};
-  if (col < cols) Vec8<T>::load(x + row * ldx + col, v);
-  const float a = max16(amax8(v));
-  if (col >= cols) return;
-  *reinterpret_cast<uint2 *>(q + row * ldq + col) = quant8<T>(v, Quant(a));
-  if ((lane & 15) == 0) s[(int64_t)(col >> 7) * lds + row] = __fdiv_rn(a, kMax);
+  const int col = (int)(blockIdx.x % segs) * 256 + lane * 8;
+  const int64_t row0 = (int64_t)(blockIdx.x / segs) * 32 + (threadIdx.x >> 5) * 4;
+  Raw8<T> raw[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (row0 + i < rows && col < cols) raw[i].load(x + (row0 + i) * ldx + col);
+  float mine = 0.f;  // the maximum whose scale this lane stores
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (row0 + i >= rows) break;
+    const float a = max16(col < cols ? raw[i].amax() : 0.f);
+    if ((lane & 15) == i) mine = a;
+    if (col < cols) {
+      float v[8];
+      raw[i].get(v);
+      *reinterpret_cast<uint2 *>(q + (row0 + i) * ldq + col) = quant8<T>(v, Quant(a));
+    }
+  }
+  const int kb = (int)(blockIdx.x % segs) * 2 + (lane >> 4), i = lane & 15;
+  if (i < 4 && row0 + i < rows && kb * kBlock < cols) s[(int64_t)kb * lds + row0 + i] = __fdiv_rn(mine, kMax);
 }
 
-// 128 x 128 blocks: one CTA per block, held in registers between the
-// reduction and the codes (16 lanes across, 16 rows per pass, 8 passes).
+// 128 x 128 blocks: one CTA per block, held in registers as loaded between the
+// reduction and the codes (16 lanes across, 32 rows per pass, 4 passes).
 template <typename T>
-__global__ void __launch_bounds__(256) quant_tiles_kernel(const T *__restrict__ x, int64_t ldx, uint8_t *__restrict__ q,
-                                                          int64_t ldq, float *__restrict__ s, int64_t lds, int rows,
-                                                          int cols) {
-  __shared__ float sh[32];
-  const int kbs = (cols + kBlock - 1) / kBlock;
-  const int nb = blockIdx.x / kbs, kb = blockIdx.x % kbs;
-  const int col = kb * kBlock + (threadIdx.x & 15) * 8;
-  float v[8][8];
+__global__ void __launch_bounds__(512, sizeof(T) == 2 ? 3 : 2)
+    quant_tiles_kernel(const T *__restrict__ x, int64_t ldx, uint8_t *__restrict__ q, int64_t ldq,
+                       float *__restrict__ s, int64_t lds, int rows, int cols, unsigned kbs) {
+  __shared__ float sh[16];
+  const unsigned nb = blockIdx.x / kbs, kb = blockIdx.x % kbs;
+  const int col = (int)kb * kBlock + (threadIdx.x & 15) * 8;
+  const int64_t row0 = (int64_t)nb * kBlock + (threadIdx.x >> 4);
+  Raw8<T> raw[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (row0 + 32 * i < rows && col < cols) raw[i].load(x + (row0 + 32 * i) * ldx + col);
   float a = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int64_t row = (int64_t)nb * kBlock + (threadIdx.x >> 4) + 16 * i;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
-    if (row < rows && col < cols) Vec8<T>::load(x + row * ldx + col, v[i]);
-    a = fmaxf(a, amax8(v[i]));
-  }
-  a = block_max(a, sh);
+  for (int i = 0; i < 4; ++i)
+    if (row0 + 32 * i < rows && col < cols) a = fmaxf(a, raw[i].amax());
+  a = warp_max(a);
+  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = a;
+  __syncthreads();
+  a = warp_max(sh[threadIdx.x & 15]);
   const Quant z(a);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int64_t row = (int64_t)nb * kBlock + (threadIdx.x >> 4) + 16 * i;
-    if (row < rows && col < cols) *reinterpret_cast<uint2 *>(q + row * ldq + col) = quant8<T>(v[i], z);
-  }
+  for (int i = 0; i < 4; ++i)
+    if (row0 + 32 * i < rows && col < cols) {
+      float v[8];
+      raw[i].get(v);
+      *reinterpret_cast<uint2 *>(q + (row0 + 32 * i) * ldq + col) = quant8<T>(v, z);
+    }
   if (threadIdx.x == 0) s[(int64_t)nb * lds + kb] = __fdiv_rn(a, kMax);
 }
 
 // ------------------------------- host side -------------------------------
 
+template <typename T, bool kRes>
+inline cudaError_t launch_norm(const T *x, const T *res, T *x_out, uint8_t *q, float *s, int64_t lds, float *r, int M,
+                               int C, cudaStream_t st) {
+  // bf16 rows of up to 2048 values take a warp each once there are enough of
+  // them to fill the SMs (1280 wide, us: 2048 rows 5.9 against 6.6 with four
+  // warps, 32,768 rows 49.1 against 54.9; 256 rows 4.6 against 3.6).  fp32 rows
+  // do not fit one warp's registers as well (4096 x 2048: 39.7 against 21.7).
+  if constexpr (sizeof(T) == 2) {
+    if (M >= 2048 && C <= 2048) {
+      const unsigned grid = rows_grid(M, 8);
+      switch ((C / 8 + 31) / 32) {
+        case 1: add_rmsnorm_fp8_kernel<T, 1, 1, kRes><<<grid, 256, 0, st>>>(x, res, x_out, q, s, lds, r, M, C); break;
+        case 2: add_rmsnorm_fp8_kernel<T, 2, 1, kRes><<<grid, 256, 0, st>>>(x, res, x_out, q, s, lds, r, M, C); break;
+        case 3: add_rmsnorm_fp8_kernel<T, 3, 1, kRes><<<grid, 256, 0, st>>>(x, res, x_out, q, s, lds, r, M, C); break;
+        case 4: add_rmsnorm_fp8_kernel<T, 4, 1, kRes><<<grid, 256, 0, st>>>(x, res, x_out, q, s, lds, r, M, C); break;
+        case 5: add_rmsnorm_fp8_kernel<T, 5, 1, kRes><<<grid, 256, 0, st>>>(x, res, x_out, q, s, lds, r, M, C); break;
+        case 6: add_rmsnorm_fp8_kernel<T, 6, 1, kRes><<<grid, 256, 0, st>>>(x, res, x_out, q, s, lds, r, M, C); break;
+        case 7: add_rmsnorm_fp8_kernel<T, 7, 1, kRes><<<grid, 256, 0, st>>>(x, res, x_out, q, s, lds, r, M, C); break;
+        default: add_rmsnorm_fp8_kernel<T, 8, 1, kRes><<<grid, 256, 0, st>>>(x, res, x_out, q, s, lds, r, M, C); break;
+      }
+      return cudaGetLastError();
+    }
+  }
+  const unsigned grid = rows_grid(M, 2);
+  switch ((C / 8 + 127) / 128) {
+    case 1: add_rmsnorm_fp8_kernel<T, 1, 4, kRes><<<grid, 256, 0, st>>>(x, res, x_out, q, s, lds, r, M, C); break;
+    case 2: add_rmsnorm_fp8_kernel<T, 2, 4, kRes><<<grid, 256, 0, st>>>(x, res, x_out, q, s, lds, r, M, C); break;
+    case 3: add_rmsnorm_fp8_kernel<T, 3, 4, kRes><<<grid, 256, 0, st>>>(x, res, x_out, q, s, lds, r, M, C); break;
+    default: add_rmsnorm_fp8_kernel<T, 4, 4, kRes><<<grid, 256, 0, st>>>(x, res, x_out, q, s, lds, r, M, C); break;
+  }
+  return cudaGetLastError();
+}
+
 template <typename T>
 inline cudaError_t launch_add_rmsnorm(const T *x, const T *res, T *x_out, uint8_t *q, float *s, int64_t lds, float *r,
                                       int M, int C, cudaStream_t st) {
-  const unsigned grid = rows_grid(M, 8);
-  if (res)
-    NC_DISPATCH_NV(C, (add_rmsnorm_fp8_kernel<T, NV, true><<<grid, 256, 0, st>>>(x, res, x_out, q, s, lds, r, M, C)));
-  else
-    NC_DISPATCH_NV(C, (add_rmsnorm_fp8_kernel<T, NV, false><<<grid, 256, 0, st>>>(x, res, x_out, q, s, lds, r, M, C)));
-  return cudaGetLastError();
+  return res ? launch_norm<T, true>(x, res, x_out, q, s, lds, r, M, C, st)
+             : launch_norm<T, false>(x, res, x_out, q, s, lds, r, M, C, st);
 }
 
 template <typename T>
 inline cudaError_t launch_quant(const T *x, int64_t ldx, uint8_t *q, int64_t ldq, float *s, int64_t lds, int rows,
                                 int cols, int block_rows, cudaStream_t st) {
-  const int64_t units = block_rows == 1 ? ((int64_t)rows * ((cols + 255) / 256) + 7) / 8
-                                        : (((int64_t)rows + 127) / 128) * ((cols + 127) / 128);
+  const unsigned across = block_rows == 1 ? (cols + 255) / 256 : (cols + 127) / 128;
+  const int64_t units = ((int64_t)rows + (block_rows == 1 ? 31 : 127)) / (block_rows == 1 ? 32 : 128) * across;
   if (units > INT32_MAX) return cudaErrorInvalidValue;
-  if (block_rows == 1) quant_rows_kernel<T><<<(unsigned)units, 256, 0, st>>>(x, ldx, q, ldq, s, lds, rows, cols);
-  else quant_tiles_kernel<T><<<(unsigned)units, 256, 0, st>>>(x, ldx, q, ldq, s, lds, rows, cols);
+  if (block_rows == 1) quant_rows_kernel<T><<<(unsigned)units, 256, 0, st>>>(x, ldx, q, ldq, s, lds, rows, cols, across);
+  else quant_tiles_kernel<T><<<(unsigned)units, 512, 0, st>>>(x, ldx, q, ldq, s, lds, rows, cols, across);
   return cudaGetLastError();
 }
 
