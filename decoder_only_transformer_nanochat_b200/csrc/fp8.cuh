@@ -121,7 +121,7 @@ __device__ __forceinline__ float max16(float a) {
 template <typename T> struct Raw8;  // eight values as loaded
 template <> struct Raw8<bf16> {
   uint4 u;
-  __device__ __forceinline__ void load(const bf16 *p) { u = __ldcs(reinterpret_cast<const uint4 *>(p)); }
+  __device__ __forceinline__ void load(const bf16 *p) { u = *reinterpret_cast<const uint4 *>(p); }
   __device__ __forceinline__ float amax() const {  // largest magnitude, two at a time
     const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&u);
     const __nv_bfloat162 m = __hmax2(__hmax2(__habs2(h[0]), __habs2(h[1])), __hmax2(__habs2(h[2]), __habs2(h[3])));
@@ -139,8 +139,8 @@ template <> struct Raw8<bf16> {
 template <> struct Raw8<float> {
   float4 a, b;
   __device__ __forceinline__ void load(const float *p) {
-    a = __ldcs(reinterpret_cast<const float4 *>(p));
-    b = __ldcs(reinterpret_cast<const float4 *>(p + 4));
+    a = *reinterpret_cast<const float4 *>(p);
+    b = *reinterpret_cast<const float4 *>(p + 4);
   }
   __device__ __forceinline__ float amax() const {
     return fmaxf(fmaxf(fmaxf(fabsf(a.x), fabsf(a.y)), fmaxf(fabsf(a.z), fabsf(a.w))),

@@ -124,18 +124,24 @@ __device__ __forceinline__ float softcap8(float z) {
 // Each owns TN / splits of the activation rows and receives the others' sums
 // for them in its shared memory; after one cluster barrier it adds them in
 // rank order (the bits do not depend on which CTA ends first) and stores.
-template <int TN> struct RowsCfg {
+//
+// kMany: more tiles than two CTAs per SM hold at once (the logits of a few
+// rows), so K is not cut; four smaller CTAs per SM then keep every tile's
+// loads in flight from the start.
+template <int TN, bool kMany> struct RowsCfg {
   static constexpr int kEpiWarps = TN > 64 ? 8 : 4;        // 4 cover the 128 TMEM lanes; 8: two column halves
   static constexpr int kCols = TN * 4 / kEpiWarps;         // activation rows per thread
   static constexpr int kThreads = 64 + 32 * kEpiWarps;
   static constexpr int kStageBytes = (128 + TN) * BK;
-  static constexpr int kCtas = TN > 64 ? 1 : 2;            // per SM
-  static constexpr int kStages = TN == 32 ? 4 : TN == 64 ? 3 : TN == 16 ? 5 : 4;
+  static constexpr int kCtas = kMany ? 4 : TN > 64 ? 1 : 2;  // per SM
+  static constexpr int kStages = kMany ? 3 : TN == 16 ? 5 : TN == 64 ? 3 : 4;
   static constexpr int kAccs = 4;                          // TMEM accumulators in flight
   static constexpr int kTmemCols = kAccs * TN;             // 64, 128, 256, 512: a power of two
   static constexpr int kScaleBytes = kEpiWarps * kCols * 4;
-  static constexpr int kSumBytes = TN * 128 * 4;           // the cluster's sums of this CTA's activation rows
+  // the cluster's sums of this CTA's activation rows; without a cluster they take the ring's memory
+  static constexpr int kSumBytes = kMany ? 0 : TN * 128 * 4;
   static constexpr int kSmem = kStages * kStageBytes + kSumBytes + kScaleBytes + 256 + 1024;
+  static_assert(!kMany || TN * 128 * 4 <= kStages * kStageBytes, "the sums fit the ring");
   // no more CTAs fit an SM than its TMEM serves: an allocation never waits for another CTA's
   static_assert(kCtas * (kSmem + 1024) <= 233472 && (kCtas + 1) * (kSmem + 1024) > 233472 && kCtas * kTmemCols <= 512,
                 "CTAs per SM");
@@ -232,16 +238,16 @@ __device__ __forceinline__ void st_cluster(uint32_t addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
-template <int TN>
-__global__ void __launch_bounds__(RowsCfg<TN>::kThreads, RowsCfg<TN>::kCtas)
+template <int TN, bool kMany>
+__global__ void __launch_bounds__(RowsCfg<TN, kMany>::kThreads, RowsCfg<TN, kMany>::kCtas)
     gemm_fp8_rows_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
                          const RowsParams p) {
-  using Cfg = RowsCfg<TN>;
+  using Cfg = RowsCfg<TN, kMany>;
   constexpr int S = Cfg::kStages, NA = Cfg::kAccs, COLS = Cfg::kCols;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  float *sums = reinterpret_cast<float *>(smem + S * Cfg::kStageBytes);  // [splits][TN / splits][128]
-  float *scales = sums + Cfg::kSumBytes / 4;
+  float *sums = reinterpret_cast<float *>(smem + (kMany ? 0 : S * Cfg::kStageBytes));  // [splits][TN / splits][128]
+  float *scales = reinterpret_cast<float *>(smem + S * Cfg::kStageBytes + Cfg::kSumBytes);
   uint64_t *bars = reinterpret_cast<uint64_t *>(scales + Cfg::kScaleBytes / 4);
   // bars: full[S], empty[S], tfull[NA], tempty[NA], drain
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * S + 2 * NA + 1);
@@ -401,18 +407,31 @@ __global__ void __launch_bounds__(RowsCfg<TN>::kThreads, RowsCfg<TN>::kCtas)
         }
       if (++acc == NA) { acc = 0; acc_phase ^= 1; }
     }
-    cluster_started(p.splits);
-    // to the CTA that owns the activation row
-    const int per = TN / p.splits;  // a power of two
-    const int shift = 31 - __clz(per);
-    const uint32_t to = smem_u32(sums) + (rank * per * 128 + row) * 4;
+    if constexpr (kMany) {
+      // The last accumulator is complete, so every MMA has read the ring and
+      // every copy has landed; after an abort one may not have: no sums then.
+      if (!*abort_flag) {
 #pragma unroll
-    for (int i = 0; i < COLS; ++i) {
-      const int c = c0 + i;
-      if (m0 + c < p.out.M) {
-        float lo, hi;
-        f2split(sum[i / 2], lo, hi);
-        st_cluster(cluster_addr(to + (c & (per - 1)) * 512, c >> shift), (i & 1) ? hi : lo);
+        for (int i = 0; i < COLS; ++i) {
+          float lo, hi;
+          f2split(sum[i / 2], lo, hi);
+          sums[(c0 + i) * 128 + row] = (i & 1) ? hi : lo;
+        }
+      }
+    } else {
+      cluster_started(p.splits);
+      // to the CTA that owns the activation row
+      const int per = TN / p.splits;  // a power of two
+      const int shift = 31 - __clz(per);
+      const uint32_t to = smem_u32(sums) + (rank * per * 128 + row) * 4;
+#pragma unroll
+      for (int i = 0; i < COLS; ++i) {
+        const int c = c0 + i;
+        if (m0 + c < p.out.M) {
+          float lo, hi;
+          f2split(sum[i / 2], lo, hi);
+          st_cluster(cluster_addr(to + (c & (per - 1)) * 512, c >> shift), (i & 1) ? hi : lo);
+        }
       }
     }
   }
@@ -474,8 +493,23 @@ static_assert(128 * 256 * 4 <= PSTAGES * PSTAGE_BYTES, "a split's sums fit the r
 // A TMA store writes whole 16-byte units of a row (measured: one byte per
 // element, N % 16 == 8, wrote eight bytes past N), so the map of D ends at the
 // last whole unit, column n_tma, and the threads take the rest of their row.
+// Division of numbers below 2^31 by a number known on the host, as a multiply
+// by its rounded-up reciprocal (Granlund and Montgomery, "Division by invariant
+// integers using multiplication"): every tile's epilogue waits for its place.
+struct ByHost {
+  uint32_t mul;
+  int shift;
+  __host__ explicit ByHost(uint32_t d = 1) {
+    shift = 31;
+    while ((1ull << (shift - 31)) < d) ++shift;
+    mul = (uint32_t)(((1ull << shift) + d - 1) / d);
+  }
+  __device__ __forceinline__ uint32_t div(uint32_t u) const { return (uint32_t)(((uint64_t)u * mul) >> shift); }
+};
+
 struct PairParams {
   Out out;
+  ByHost by_n, by_group;  // n_n, 16 n_n
   int kblocks, splits;  // pairs per cluster
   int n_m, n_n, units, n_tma;
   const float *sa, *sb;
@@ -531,15 +565,16 @@ __device__ __forceinline__ void mma8_pair(uint32_t d_tmem, uint64_t adesc, uint6
 
 // Tiles in flight at once share operand panels in L2: with few N tiles those
 // of an M block are consecutive, with many 16 M blocks share each B panel.
-__device__ __forceinline__ void pair_tile(const PairParams &p, int u, int &m_blk, int &n_blk) {
+__device__ __forceinline__ void pair_tile(const PairParams &p, uint32_t u, int &m_blk, int &n_blk) {
   if (p.n_n <= 16) {
-    m_blk = u / p.n_n;
-    n_blk = u % p.n_n;
+    m_blk = p.by_n.div(u);
+    n_blk = u - m_blk * p.n_n;
     return;
   }
-  const int G = 16, per = G * p.n_n, first = u / per * G, size = min(p.n_m - first, G), r = u % per;
-  m_blk = first + r % size;
-  n_blk = r / size;
+  const uint32_t g = p.by_group.div(u), r = u - g * 16 * p.n_n;
+  const int first = g * 16, size = min(p.n_m - first, 16);
+  n_blk = size == 16 ? r / 16 : r / size;
+  m_blk = first + r - n_blk * size;
 }
 
 template <int EPI>
@@ -966,9 +1001,9 @@ inline bool make_map8(CUtensorMap *map, const void *base, int64_t rows, int64_t 
 
 inline Out out_of(const GemmFp8Problem &g) { return Out{g.M, g.N, g.D, g.ldd, g.sd, g.lsd}; }
 
-template <int TN>
+template <int TN, bool kMany>
 inline cudaError_t launch_rows(const GemmFp8Problem &g, int num_sms, int *status, cudaStream_t st) {
-  using Cfg = RowsCfg<TN>;
+  using Cfg = RowsCfg<TN, kMany>;
   CUtensorMap mw, mx;
   if (!make_map8(&mw, g.B, g.N, g.K, g.ldb, 128) || !make_map8(&mx, g.A, g.M, g.K, g.lda, TN)) return cudaErrorInvalidValue;
   RowsParams p;
@@ -980,7 +1015,7 @@ inline cudaError_t launch_rows(const GemmFp8Problem &g, int num_sms, int *status
   const int64_t tiles = (int64_t)p.n_m * ((g.N + 127) / 128);
   // cut K while every CTA still finds a place at once and keeps a K block
   p.splits = 1;
-  while (p.splits < 8 && 2 * p.splits <= p.kblocks && tiles * 2 * p.splits <= Cfg::kCtas * num_sms) p.splits *= 2;
+  while (!kMany && p.splits < 8 && 2 * p.splits <= p.kblocks && tiles * 2 * p.splits <= Cfg::kCtas * num_sms) p.splits *= 2;
   if (tiles * p.splits > INT32_MAX) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(tiles * p.splits));
@@ -994,7 +1029,7 @@ inline cudaError_t launch_rows(const GemmFp8Problem &g, int num_sms, int *status
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = p.splits > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, gemm_fp8_rows_kernel<TN>, mw, mx, p);
+  return cudaLaunchKernelEx(&cfg, gemm_fp8_rows_kernel<TN, kMany>, mw, mx, p);
 }
 
 inline cudaError_t launch_pair(const GemmFp8Problem &g, int num_sms, int *status, cudaStream_t st) {
@@ -1022,6 +1057,8 @@ inline cudaError_t launch_pair(const GemmFp8Problem &g, int num_sms, int *status
   p.n_n = (g.N + 255) / 256;
   if ((int64_t)p.n_m * p.n_n > INT32_MAX / 2) return cudaErrorInvalidValue;  // unit + grid stays an int
   p.units = p.n_m * p.n_n;
+  p.by_n = ByHost(p.n_n);
+  p.by_group = ByHost(16u * p.n_n);
   p.sa = g.sa; p.lsa = g.lsa; p.sb = g.sb; p.lsb = g.lsb;
   p.status = status;
   p.splits = 1;
@@ -1057,10 +1094,11 @@ inline cudaError_t init() {
   auto big = [&](auto *k, int bytes) {
     if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   };
-  big(gemm_fp8_rows_kernel<16>, RowsCfg<16>::kSmem);
-  big(gemm_fp8_rows_kernel<32>, RowsCfg<32>::kSmem);
-  big(gemm_fp8_rows_kernel<64>, RowsCfg<64>::kSmem);
-  big(gemm_fp8_rows_kernel<128>, RowsCfg<128>::kSmem);
+  big(gemm_fp8_rows_kernel<16, true>, RowsCfg<16, true>::kSmem);
+  big(gemm_fp8_rows_kernel<16, false>, RowsCfg<16, false>::kSmem);
+  big(gemm_fp8_rows_kernel<32, false>, RowsCfg<32, false>::kSmem);
+  big(gemm_fp8_rows_kernel<64, false>, RowsCfg<64, false>::kSmem);
+  big(gemm_fp8_rows_kernel<128, false>, RowsCfg<128, false>::kSmem);
   auto pair = [&](auto *k) {
     big(k, PSMEM);
     cudaFuncAttributes a;
@@ -1079,17 +1117,17 @@ inline cudaError_t init() {
 }  // namespace tc8
 
 inline cudaError_t launch_gemm_fp8(const GemmFp8Problem &g, int num_sms, int *status, cudaStream_t st) {
-#ifndef PAIRM
-#define PAIRM 256
-#endif
-  if (g.M > PAIRM) return tc8::launch_pair(g, num_sms, status, st);
-  if (g.M <= 16) return tc8::launch_rows<16>(g, num_sms, status, st);
-  if (g.M <= 32) return tc8::launch_rows<32>(g, num_sms, status, st);
-#ifndef M64
-#define M64 64
-#endif
-  if (g.M <= M64) return tc8::launch_rows<64>(g, num_sms, status, st);
-  return tc8::launch_rows<128>(g, num_sms, status, st);
+  // 256-row tiles from 257 rows on, and from 65 on where 128-row tiles leave no
+  // room to cut K (256 x 5120 x 1280: PAIRNOTE)
+  const int64_t across = ((int64_t)g.N + 127) / 128;
+  if (g.M > 256 || (g.M > 64 && 2 * across * ((g.M + 127) / 128) > num_sms))
+    return tc8::launch_pair(g, num_sms, status, st);
+  // the logits of a few rows (16 x 65,536 x 1280: 21.2 us with four CTAs per SM, 24.9 with two)
+  if (g.M <= 16 && across > 2 * num_sms) return tc8::launch_rows<16, true>(g, num_sms, status, st);
+  if (g.M <= 16) return tc8::launch_rows<16, false>(g, num_sms, status, st);
+  if (g.M <= 32) return tc8::launch_rows<32, false>(g, num_sms, status, st);
+  if (g.M <= 64) return tc8::launch_rows<64, false>(g, num_sms, status, st);
+  return tc8::launch_rows<128, false>(g, num_sms, status, st);
 }
 
 }  // namespace nc

@@ -353,6 +353,7 @@ SHAPES = [
     (300, 1003, 272), (290, 5, 144), (513, 385, 130), (300, 262, 16),   # N that no 16-byte unit divides
     (270, 300, 3200), (400, 1003, 6416),   # K cut over two and four pairs of CTAs
     (40, 20485, 144),      # many weight tiles
+    (16, 40003, 272), (5, 38400, 1040),   # more tiles than two CTAs per SM hold
 ]
 
 
