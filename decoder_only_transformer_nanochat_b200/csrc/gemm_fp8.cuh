@@ -56,9 +56,10 @@ __device__ __forceinline__ void mma8(uint32_t d_tmem, uint64_t adesc, uint64_t b
       : "memory");
 }
 // Bounded wait for barriers that are handed over every K block: a count of
-// tries is the limit (a fraction of a second at least), which costs the
-// callers one register where a clock would cost several.
-constexpr uint32_t kTries = 1u << 24;
+// tries is the limit, which costs the callers one register where a clock would
+// cost several.  A try gives up after 2 us (measured), so 2^21 of them are
+// four seconds without progress.
+constexpr uint32_t kTries = 1u << 21;
 __device__ __forceinline__ bool wait8(uint32_t bar, uint32_t parity, volatile int *abort_flag, int *status) {
   for (uint32_t i = 1; !mbar_try(bar, parity); ++i) {
     if ((i & 255) == 0 && (*abort_flag || i > kTries)) {
@@ -609,6 +610,11 @@ __global__ void __launch_bounds__(PTHREADS, 1)
   const uint32_t drain_bar = smem_u32(bars + 3 * S + 4);
   auto aux_bar = [&](int w) { return smem_u32(bars + 3 * S + 5 + w); };
 
+  if (threadIdx.x == 32) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_a)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_b)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_d)) : "memory");
+  }
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(full_bar(s), 1);
@@ -1118,7 +1124,8 @@ inline cudaError_t init() {
 
 inline cudaError_t launch_gemm_fp8(const GemmFp8Problem &g, int num_sms, int *status, cudaStream_t st) {
   // 256-row tiles from 257 rows on, and from 65 on where 128-row tiles leave no
-  // room to cut K (256 x 5120 x 1280: PAIRNOTE)
+  // room to cut K (256 x 5120 x 1280: 12.2 us against 17.1; 96 x 1280 x 5120: 16.9
+  // against 12.7 with 128-row tiles)
   const int64_t across = ((int64_t)g.N + 127) / 128;
   if (g.M > 256 || (g.M > 64 && 2 * across * ((g.M + 127) / 128) > num_sms))
     return tc8::launch_pair(g, num_sms, status, st);

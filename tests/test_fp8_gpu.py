@@ -351,6 +351,7 @@ SHAPES = [
     (200, 1003, 656), (300, 520, 1040), (515, 776, 1296), (1030, 264, 272), (270, 200, 8208),
     (20485, 392, 272),     # several tiles per pair of CTAs, the last column half of 8 columns
     (300, 1003, 272), (290, 5, 144), (513, 385, 130), (300, 262, 16),   # N that no 16-byte unit divides
+    (100, 10241, 400), (256, 9600, 272),   # 256-row tiles for fewer rows
     (270, 300, 3200), (400, 1003, 6416),   # K cut over two and four pairs of CTAs
     (40, 20485, 144),      # many weight tiles
     (16, 40003, 272), (5, 38400, 1040),   # more tiles than two CTAs per SM hold
@@ -363,6 +364,151 @@ def test_gemm(nc, M, N, K):
     refs = (c["av"] @ c["bv"].T, _acc_bound(c["av"], c["bv"]))
     for epi in EPIS:
         _check(nc, c, epi, refs)
+
+
+def _random_case(i):
+    """Sizes over the whole range, small ones as often as large (no size is special to a kernel)."""
+    r = np.random.RandomState(1000 + i)
+    M = int(np.exp(r.uniform(0, np.log(1500))))
+    N = int(np.exp(r.uniform(0, np.log(4000))))
+    K = int(np.exp(r.uniform(0, np.log(5000))))
+    return M, N, K, EPIS[i % len(EPIS)]
+
+
+@pytest.mark.parametrize("i", range(48))
+def test_gemm_random_sizes(nc, i):
+    M, N, K, epi = _random_case(i)
+    c = _case(nc, M, N, K, seed=i, pad=16 * (i % 3))
+    _check(nc, c, epi)
+
+
+@pytest.mark.parametrize("M,N", [(1, 40), (70, 300), (300, 520)])
+def test_gemm_zero_blocks(nc, M, N):
+    """Rows and weight blocks of zeros (scale 0) give zeros, in 8 bits too."""
+    import torch
+    c = _case(nc, M, N, 400)
+    c["a"].view(torch.uint8)[0] = 0
+    c["sa"][:, 0] = 0
+    D = torch.full((M, 16 * -(-N // 16)), 3.0, device="cuda").bfloat16()
+    assert _gemm(nc, c, "STORE", D, D.shape[1]) == 0
+    assert (D[0, :N] == 0).all() and (D[1:, :N] != 0).any() == (M > 1)
+    q = torch.full((M, 16 * -(-N // 16)), 3.0, device="cuda").to(torch.float8_e4m3fn)
+    sd = torch.full((_blocks(N), M), 5.0, device="cuda")
+    assert _gemm(nc, c, "RELU2_FP8", q, q.shape[1], sd, M) == 0
+    assert (q.float()[0, :N] == 0).all() and (sd[:, 0] == 0).all()
+    # a product that is negative everywhere: relu^2 leaves zeros
+    c["a"].view(torch.uint8).fill_(0x38)      # 1
+    c["b"].view(torch.uint8).fill_(0xb8)      # -1
+    c["sa"].fill_(0.5)
+    c["sb"].fill_(0.25)
+    assert _gemm(nc, c, "RELU2_FP8", q, q.shape[1], sd, M) == 0
+    assert (q.float()[:, :N] == 0).all() and (sd == 0).all()
+    assert _gemm(nc, c, "STORE", D, D.shape[1]) == 0
+    assert (D[:, :N] == -50).all()            # 400 products of -1/8, exact
+
+
+@pytest.mark.parametrize("M,N", [(9, 200), (300, 300)])
+def test_gemm_tiny_and_huge_scales(nc, M, N):
+    """Sums far from 1: an 8-bit output of sums near 2^-70 (their squares near 2^-140, below any normal
+    number's square root) and of sums near 2^50."""
+    import torch
+    K = 256
+    c = _case(nc, M, N, K)
+    sa0 = c["sa"].clone()
+    for e in (-50, 50):
+        c["sa"].copy_(sa0 * 2.0 ** e)
+        D = torch.zeros(M, 16 * -(-N // 16), device="cuda").to(torch.float8_e4m3fn)
+        sd = torch.zeros(_blocks(N), M, device="cuda")
+        assert _gemm(nc, c, "RELU2_FP8", D, D.shape[1], sd, M) == 0
+        acc = (c["av"] * 2.0 ** e) @ c["bv"].T
+        v = np.maximum(acc, 0) ** 2
+        _, ea = _acc_bound(c["av"] * 2.0 ** e, c["bv"])
+        ev = 2 * np.abs(acc) * ea + ea * ea + U * v
+        s = _host(sd)
+        sx = _expand(s, M, N, 1)
+        # scales below 2^-126 have steps of 2^-149
+        tol = ev + _expand(_block_max(ev, 1), M, N, 1) + np.maximum(2.0 ** -4 * (v + ev), 2.0 ** -10 * sx) * (1 + 8 * U)
+        assert (np.abs(_host(D)[:, :N] * sx - v) <= tol + 448 * 2.0 ** -149).all()
+
+
+def test_offsets_past_32_bits(nc):
+    """Rows that start past 2^31 and 2^32 elements, in every operator."""
+    import torch
+    bf, e8 = torch.bfloat16, torch.float8_e4m3fn
+    M, C, tail = 2_200_000, 2048, 5
+    x = torch.zeros(M, C, dtype=bf, device="cuda")
+    xt, xv = _dev(_rows(11, tail, C), "bf16")
+    x[-tail:] = xt
+    cq, cs = _codes(xv, 1)
+    q = torch.zeros(M, C, dtype=e8, device="cuda")
+    s = torch.zeros(_blocks(C), M, device="cuda")
+    assert nc.nc_quant_fp8(x.data_ptr(), C, q.data_ptr(), C, s.data_ptr(), M, M, C, 1, nc.NC_BF16, _stream()) == 0
+    np.testing.assert_array_equal(_host(q[-tail:]), cq)
+    np.testing.assert_array_equal(_host(s[:, -tail:]), cs)
+    s128 = torch.zeros(-(-M // 128), _blocks(C), device="cuda")
+    q.zero_()
+    assert nc.nc_quant_fp8(x.data_ptr(), C, q.data_ptr(), C, s128.data_ptr(), _blocks(C), M, C, 128, nc.NC_BF16,
+                           _stream()) == 0
+    last = M - M % 128
+    assert M - last >= tail
+    block = np.zeros((M - last, C))
+    block[-tail:] = xv
+    bq, bs = _codes(block, 128)
+    np.testing.assert_array_equal(_host(q[last:]), bq)
+    np.testing.assert_array_equal(_host(s128[-1:]), bs)
+    assert nc.nc_add_rmsnorm_fp8(x.data_ptr(), x.data_ptr(), x.data_ptr(), q.data_ptr(), s.data_ptr(), M, None, M, C,
+                                 nc.NC_BF16, _stream()) == 0
+    np.testing.assert_array_equal(_host(x[-tail:]), 2 * xv)
+    np.testing.assert_array_equal(_host(q[-tail:]), cq)
+    del x, s128
+    # D past 2^32 elements: A = the last rows' codes in one K block, weights of one block
+    K, N = 128, 2000
+    w, sw, wv = _operand(5, N, K, 128, K)
+    swd = torch.from_numpy(sw.copy()).float().cuda()
+    a = q[:, :K]
+    D = torch.empty(M, N, dtype=bf, device="cuda")
+    s1 = s[:1].contiguous()
+    assert nc.nc_gemm_fp8(a.data_ptr(), C, s1.data_ptr(), M, w.data_ptr(), K, swd.data_ptr(), 1, D.data_ptr(), N, None, 0,
+                          M, N, K, nc.NC_EPI_STORE, _stream()) == 0
+    assert nc.nc_ops_status(_stream(), 60000) == 0
+    av = _host(a[-tail:]) * _host(s1[:, -tail:]).T
+    ref, (_, e) = av @ wv.T, _acc_bound(av, wv)
+    got = _host(D[-tail:])
+    assert (np.abs(got - ref) <= e + 2.0 ** -8 * (np.abs(ref) + e)).all()
+    assert (D[:-tail:99991] == 0).all()
+
+
+def test_calls_on_two_streams_at_once(nc):
+    """Both kinds of kernel on two streams at once, again and again: each call's bits are those of the call alone."""
+    import torch
+    shapes = [(900, 1300, 1040, "STORE"), (5, 2000, 2048, "RELU2"), (40, 700, 1300, "STORE_F32"), (300, 600, 6416, "SOFTCAP"),
+              (150, 256, 2048, "STORE")]
+    cases = [(_case(nc, M, N, K), epi) for M, N, K, epi in shapes]
+
+    def out(c, epi):
+        return torch.zeros(c["M"], 16 * -(-c["N"] // 16), device="cuda",
+                           dtype=torch.float32 if epi == "STORE_F32" else torch.bfloat16)
+    want = []
+    for c, epi in cases:
+        D = out(c, epi)
+        assert _gemm(nc, c, epi, D, D.shape[1]) == 0
+        want.append(D)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[[out(c, epi) for c, epi in cases] for _ in range(4)] for _ in streams]
+    torch.cuda.synchronize()
+    for r in range(4):
+        for i in range(len(cases)):
+            for k, st in enumerate(streams):
+                j = (i + 2 * k) % len(cases)
+                c, epi = cases[j]
+                assert _gemm(nc, c, epi, got[k][r][j], got[k][r][j].shape[1], stream=st.cuda_stream) == 0
+    torch.cuda.synchronize()
+    for k in range(2):
+        for r in range(4):
+            for j, w in enumerate(want):
+                assert torch.equal(got[k][r][j], w), (k, r, j)
+    assert nc.nc_ops_status(_stream(), 60000) == 0
 
 
 def test_gemm_repeats_bit_for_bit(nc):
