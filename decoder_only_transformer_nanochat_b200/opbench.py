@@ -7,6 +7,8 @@ it every shape that grows with the tokens, so a capture holds a few GB).
     python -m decoder_only_transformer_nanochat_b200.opbench --op w1_fwd --iters 5
     python -m decoder_only_transformer_nanochat_b200.opbench --op ce --tokens 8192
     python -m decoder_only_transformer_nanochat_b200.opbench --op rmsnorm --tokens 65536
+    python -m decoder_only_transformer_nanochat_b200.opbench --op gemm_fp8 --shape 16,65536,1280,SOFTCAP
+    python -m decoder_only_transformer_nanochat_b200.opbench --op norm_fp8 --tokens 32768
 """
 from __future__ import annotations
 
@@ -39,6 +41,57 @@ def gemm_shapes(M: int) -> dict:
 
 GEMMS = gemm_shapes(16 * 2048)
 ROW_OPS = ["rmsnorm", "rmsnorm_bwd", "rope", "rope_bwd"]
+FP8_OPS = ["norm_fp8", "quant_rows_fp8", "quant_weight_fp8", "gemm_fp8"]
+
+
+def fp8_op(nc, torch, args, g, st):
+    """(run, flops, bytes) of an 8-bit operator: the norm and the row quantiser at --tokens rows of the d20 width,
+    the weight quantiser on W1, the GEMM at --shape (default: the W1 projection of --tokens rows)."""
+    e8 = torch.float8_e4m3fn
+
+    def quant(x, rows):
+        R, K = x.shape
+        q = torch.empty(R, K, device="cuda", dtype=e8)
+        s = torch.empty((-(-K // 128), R) if rows == 1 else (-(-R // 128), -(-K // 128)), device="cuda")
+
+        def call():
+            assert nc.nc_quant_fp8(x.data_ptr(), K, q.data_ptr(), K, s.data_ptr(), s.shape[1], R, K, rows, nc.NC_BF16,
+                                   st) == 0
+        call()
+        return q, s, call
+
+    def randn(*n):
+        return torch.randn(*n, device="cuda", generator=g, dtype=torch.bfloat16)
+    M = args.tokens
+    if args.op == "gemm_fp8":
+        f = (args.shape or f"{M},{F},{C},RELU2_FP8").split(",")
+        M, N, K, epi = int(f[0]), int(f[1]), int(f[2]), f[3]
+        a, sa, _ = quant(randn(M, K), 1)
+        b, sb, _ = quant(randn(N, K).mul_(K ** -0.5), 128)
+        size = {"STORE_F32": 4, "RELU2_FP8": 1}.get(epi, 2)
+        ldd = -(-N // 16) * 16
+        D = torch.zeros(M, ldd, device="cuda", dtype={1: e8, 2: torch.bfloat16, 4: torch.float32}[size])
+        sd = torch.empty(-(-N // 128), M, device="cuda")
+
+        def run():
+            assert nc.nc_gemm_fp8(a.data_ptr(), K, sa.data_ptr(), M, b.data_ptr(), K, sb.data_ptr(), sb.shape[1],
+                                  D.data_ptr(), ldd, sd.data_ptr(), M, M, N, K, getattr(nc, "NC_EPI_" + epi), st) == 0
+        moved = size * (2 if epi == "ADD" else 1)
+        return run, 2.0 * M * N * K, M * K + N * K + moved * M * N + 4.0 * (sa.numel() + sb.numel())
+    if args.op == "quant_weight_fp8":
+        _, s, run = quant(randn(F, C), 128)
+        return run, 0.0, 3.0 * F * C + 4 * s.numel()
+    x = randn(M, C)
+    if args.op == "quant_rows_fp8":
+        _, s, run = quant(x, 1)
+        return run, 0.0, 3.0 * M * C + 4 * s.numel()
+    res, out = randn(M, C), torch.empty_like(x)
+    q, s = torch.empty(M, C, device="cuda", dtype=e8), torch.empty(C // 128, M, device="cuda")
+
+    def run():
+        assert nc.nc_add_rmsnorm_fp8(x.data_ptr(), res.data_ptr(), out.data_ptr(), q.data_ptr(), s.data_ptr(), M, None, M,
+                                     C, nc.NC_BF16, st) == 0
+    return run, 0.0, 7.0 * M * C + 4 * s.numel()
 
 
 def main():
@@ -48,11 +101,11 @@ def main():
     from decoder_only_transformer_nanochat_b200 import build
     ap = argparse.ArgumentParser()
     ap.add_argument("--op", required=True,
-                    choices=sorted(GEMMS) + ["attn_fwd", "attn_bwd", "gemm", "ce"] + ROW_OPS)
+                    choices=sorted(GEMMS) + ["attn_fwd", "attn_bwd", "gemm", "ce"] + ROW_OPS + FP8_OPS)
     ap.add_argument("--tokens", type=int, default=16 * 2048, help="M (a multiple of 2048)")
     ap.add_argument("--heads", type=int, default=H, help="attention: query heads (d20: 10)")
     ap.add_argument("--window", type=int, default=0, help="attention: sliding window (0: causal)")
-    ap.add_argument("--shape", default=None, help="for --op gemm: M,N,K,a_mn,b_mn,EPILOGUE")
+    ap.add_argument("--shape", default=None, help="for --op gemm: M,N,K,a_mn,b_mn,EPILOGUE; for --op gemm_fp8: M,N,K,EPILOGUE")
     ap.add_argument("--iters", type=int, default=5)
     ap.add_argument("--engine", type=int, default=0)
     args = ap.parse_args()
@@ -68,7 +121,9 @@ def main():
     if args.op == "gemm":
         f = args.shape.split(",")
         shapes["gemm"] = (int(f[0]), int(f[1]), int(f[2]), int(f[3]), int(f[4]), f[5])
-    if args.op == "ce":
+    if args.op in FP8_OPS:
+        run, flops, nbytes = fp8_op(nc, torch, args, g, st)
+    elif args.op == "ce":
         M = args.tokens
         z = (torch.randn(M * V, device="cuda", generator=g) * 3.0).to(torch.bfloat16)
         z0 = z.clone()
@@ -202,7 +257,7 @@ def main():
         out["tflops"] = flops / (med / 1000) / 1e12
     if args.op == "ce":
         out["gbs"] = 2.0 * args.tokens * V * 2 / (med / 1000) / 1e9  # z read once, dz written once
-    if args.op in ROW_OPS:
+    if args.op in ROW_OPS + FP8_OPS:
         out["gbs"] = nbytes / (med / 1000) / 1e9  # every operand read once, every output written once
     print(json.dumps(out))
 
