@@ -688,24 +688,37 @@ __global__ void __launch_bounds__(PTHREADS, 1)
       bool ok = true;
       for (int u = cluster; u < p.units && ok; u += n_clusters) {
         for (int kb = kb0; kb < kb1; ++kb) {
-          ok = __all_sync(0xffffffffu, wait8(full_bar(stage), phase, abort_flag, p.status));
-          const uint64_t ad = desc0 + (uint64_t)(stage * (PSTAGE_BYTES >> 4));
+          // One look at all three barriers where they are ready, as they mostly
+          // are: three waits in turn cost this thread more than the MMAs take.
+          const bool f = mbar_test(full_bar(stage), phase), l = mbar_test(tempty_bar(2 * acc), acc_phase ^ 1),
+                     r = mbar_test(tempty_bar(2 * acc + 1), acc_phase ^ 1);
+          const bool ready = __all_sync(0xffffffffu, f && l && r);
+          if (!ready) {
+            ok = __all_sync(0xffffffffu, wait8(full_bar(stage), phase, abort_flag, p.status) &&
+                                             wait8(tempty_bar(2 * acc), acc_phase ^ 1, abort_flag, p.status));
+            if (!ok) break;
+          }
+          tc_fence_after();
+          const uint64_t ad = desc0 + (uint64_t)(stage * (PSTAGE_BYTES >> 4)), bd = ad + (128 * BK >> 4);
+          if (elected) {
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const int a = 2 * acc + half;
-            ok = ok && __all_sync(0xffffffffu, wait8(tempty_bar(a), acc_phase ^ 1, abort_flag, p.status));
+            for (int kk = 0; kk < BK / 32; ++kk)
+              mma8_pair(tmem_base + acc * 256, ad + 2 * kk, bd + 2 * kk, idesc, kk > 0);
+            tc_commit_pair(done_bar(stage, 0), both);
+          }
+          __syncwarp();
+          if (!ready) {
+            ok = __all_sync(0xffffffffu, wait8(tempty_bar(2 * acc + 1), acc_phase ^ 1, abort_flag, p.status));
             if (!ok) break;
             tc_fence_after();
-            const uint64_t bd = ad + ((128 + 64 * half) * BK >> 4);
-            if (elected) {
-#pragma unroll
-              for (int kk = 0; kk < BK / 32; ++kk)
-                mma8_pair(tmem_base + a * 128, ad + 2 * kk, bd + 2 * kk, idesc, kk > 0);
-              tc_commit_pair(done_bar(stage, half), both);
-            }
-            __syncwarp();
           }
-          if (!ok) break;
+          if (elected) {
+#pragma unroll
+            for (int kk = 0; kk < BK / 32; ++kk)
+              mma8_pair(tmem_base + acc * 256 + 128, ad + 2 * kk, bd + (64 * BK >> 4) + 2 * kk, idesc, kk > 0);
+            tc_commit_pair(done_bar(stage, 1), both);
+          }
+          __syncwarp();
           if (++stage == S) { stage = 0; phase ^= 1; }
           acc ^= 1;
           if (acc == 0) acc_phase ^= 1;
