@@ -478,7 +478,7 @@ __global__ void __launch_bounds__(RowsCfg<TN, kMany>::kThreads, RowsCfg<TN, kMan
 constexpr int PSTAGES = 5;
 constexpr int PSTAGE_BYTES = 2 * 128 * BK;  // A and B rows of one CTA: 32 KB
 constexpr int PEPI_WARPS = 8;
-// Three warpgroups: warp 0 TMA, warp 1 MMA (warps 2, 3 idle), warps 4..11 the
+// Three warpgroups: warp 0 TMA, warps 1 and 2 MMA (warp 3 idle), warps 4..11 the
 // epilogue, which holds 128 sums a thread.  The first gives registers to the
 // others: 128 x 24 + 256 x 240 = 64,512, all of the 384 x 168 of the launch
 // (init() checks that count), so every increase can be met.
@@ -602,7 +602,7 @@ __global__ void __launch_bounds__(PTHREADS, 1)
   const int kb1 = (int)((int64_t)p.kblocks * (split + 1) / p.splits);
   auto full_bar = [&](int s) { return smem_u32(bars + s); };
   // done[s, h]: the MMAs of stage s and column half h are complete, so that
-  // half of its accumulator is full, and with h = 1, the second, the stage is free.
+  // half of its accumulator is full, and with both the stage is free.
   // (The epilogue cannot miss a phase: the stage's next MMAs wait for an
   // accumulator that it has yet to hand back.)
   auto done_bar = [&](int s, int h) { return smem_u32(bars + S + 2 * s + h); };
@@ -622,7 +622,7 @@ __global__ void __launch_bounds__(PTHREADS, 1)
       mbar_init(done_bar(s, 1), 1);
     }
     for (int a = 0; a < 4; ++a) mbar_init(tempty_bar(a), PEPI_WARPS);  // a column half's epilogue warps of both CTAs
-    mbar_init(drain_bar, 1);
+    mbar_init(drain_bar, 2);  // both MMA warps
     for (int w = 0; w < PEPI_WARPS; ++w) mbar_init(aux_bar(w), 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -652,7 +652,8 @@ __global__ void __launch_bounds__(PTHREADS, 1)
       pair_tile(p, u, m_blk, n_blk);
       const int m_row = m_blk * 256 + (int)rank * 128, n_row = n_blk * 256 + (int)rank * 64;
       for (int kb = kb0; kb < kb1; ++kb) {
-        ok = __all_sync(0xffffffffu, wait8(done_bar(stage, 1), phase ^ 1, abort_flag, p.status));
+        ok = __all_sync(0xffffffffu, wait8(done_bar(stage, 0), phase ^ 1, abort_flag, p.status) &&
+                                         wait8(done_bar(stage, 1), phase ^ 1, abort_flag, p.status));
         if (!ok) break;
         const uint32_t sa = smem_u32(smem + stage * PSTAGE_BYTES);
         const uint32_t fb = cluster_addr(full_bar(stage), lead);
@@ -677,46 +678,28 @@ __global__ void __launch_bounds__(PTHREADS, 1)
         while (!mbar_try(full_bar(stage), phase) && globaltimer() - t0 < kWaitNs) {}
       }
     __syncwarp();
-  } else if (warp == 1) {
+  } else if (warp <= 2) {
     if (leader) {
-      // ---------------- MMA issuer ----------------
+      // ---------------- MMA issuers: warp 1 the left column half, warp 2 the right ----------------
+      const int half = warp - 1;
       const uint32_t idesc = idesc8(256, 128);
       const uint32_t elected = elect_one();
       const uint64_t desc0 = smem_desc(smem_u32(smem), 16, 1024);
+      const uint32_t d0 = tmem_base + half * 128;
       int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
       for (int u = cluster; u < p.units && ok; u += n_clusters) {
         for (int kb = kb0; kb < kb1; ++kb) {
-          // One look at all three barriers where they are ready, as they mostly
-          // are: three waits in turn cost this thread more than the MMAs take.
-          const bool f = mbar_test(full_bar(stage), phase), l = mbar_test(tempty_bar(2 * acc), acc_phase ^ 1),
-                     r = mbar_test(tempty_bar(2 * acc + 1), acc_phase ^ 1);
-          const bool ready = __all_sync(0xffffffffu, f && l && r);
-          if (!ready) {
-            ok = __all_sync(0xffffffffu, wait8(full_bar(stage), phase, abort_flag, p.status) &&
-                                             wait8(tempty_bar(2 * acc), acc_phase ^ 1, abort_flag, p.status));
-            if (!ok) break;
-          }
+          ok = __all_sync(0xffffffffu, wait8(full_bar(stage), phase, abort_flag, p.status) &&
+                                           wait8(tempty_bar(2 * acc + half), acc_phase ^ 1, abort_flag, p.status));
+          if (!ok) break;
           tc_fence_after();
-          const uint64_t ad = desc0 + (uint64_t)(stage * (PSTAGE_BYTES >> 4)), bd = ad + (128 * BK >> 4);
+          const uint64_t ad = desc0 + (uint64_t)(stage * (PSTAGE_BYTES >> 4)), bd = ad + ((128 + 64 * half) * BK >> 4);
           if (elected) {
 #pragma unroll
-            for (int kk = 0; kk < BK / 32; ++kk)
-              mma8_pair(tmem_base + acc * 256, ad + 2 * kk, bd + 2 * kk, idesc, kk > 0);
-            tc_commit_pair(done_bar(stage, 0), both);
-          }
-          __syncwarp();
-          if (!ready) {
-            ok = __all_sync(0xffffffffu, wait8(tempty_bar(2 * acc + 1), acc_phase ^ 1, abort_flag, p.status));
-            if (!ok) break;
-            tc_fence_after();
-          }
-          if (elected) {
-#pragma unroll
-            for (int kk = 0; kk < BK / 32; ++kk)
-              mma8_pair(tmem_base + acc * 256 + 128, ad + 2 * kk, bd + (64 * BK >> 4) + 2 * kk, idesc, kk > 0);
-            tc_commit_pair(done_bar(stage, 1), both);
+            for (int kk = 0; kk < BK / 32; ++kk) mma8_pair(d0 + acc * 256, ad + 2 * kk, bd + 2 * kk, idesc, kk > 0);
+            tc_commit_pair(done_bar(stage, half), both);
           }
           __syncwarp();
           if (++stage == S) { stage = 0; phase ^= 1; }
@@ -839,7 +822,7 @@ __global__ void __launch_bounds__(PTHREADS, 1)
       if (!ok) break;
       if (p.splits > 1) {  // the cluster's only tile: its sums go to shared memory
         const int last = stage ? stage - 1 : S - 1;
-        ok = __all_sync(0xffffffffu, wait8(done_bar(last, 1), stage ? phase : phase ^ 1, abort_flag, p.status));
+        ok = __all_sync(0xffffffffu, wait8(done_bar(last, cg ^ 1), stage ? phase : phase ^ 1, abort_flag, p.status));
         if (!ok) break;
         // no MMA reads the ring and no copy is on its way to it any more
         const int row = quarter * 32 + lane;

@@ -1426,6 +1426,8 @@ int nc_gemm_fp8(const void *A, int64_t lda, const float *sa, int64_t lsa, const 
   const int most = 1 << 30;
   if (M < 1 || N < 1 || K < 1 || M > most || N > most || K > most) return NC_ESHAPE;
   if (lda < K || ldb < K || ldd < N || lsa < M || lsb < (K + 127) / 128 || (f8 && lsd < M)) return NC_ESHAPE;
+  const int64_t far = (int64_t)1 << 38;  // row strides the tensor maps hold (2^40 bytes)
+  if (lda >= far || ldb >= far || ldd >= far) return NC_ESHAPE;
   if ((((uintptr_t)A | (uintptr_t)B | (uintptr_t)D) & 15) || (((uintptr_t)sa | (uintptr_t)sb) & 3) ||
       (f8 && ((uintptr_t)sd & 3)) || lda % 16 || ldb % 16 || ldd % (f8 ? 16 : f32 ? 4 : 8))
     return NC_EALIGN;

@@ -58,7 +58,7 @@ def test_gemm_refusals():
         assert _gemm(epi=epi) == nc.NC_EINVAL
     assert _gemm(epi=nc.NC_EPI_RELU2_FP8, sd=None) == nc.NC_EINVAL
     for bad in (dict(M=0), dict(N=0), dict(K=0), dict(M=-4), dict(lda=240), dict(ldb=240), dict(ldd=56), dict(lsa=7),
-                dict(lsb=1), dict(epi=nc.NC_EPI_RELU2_FP8, lsd=7), dict(M=(1 << 30) + 1, lsa=1 << 31)):
+                dict(lsb=1), dict(epi=nc.NC_EPI_RELU2_FP8, lsd=7), dict(M=(1 << 30) + 1, lsa=1 << 31), dict(lda=1 << 38), dict(ldd=1 << 38)):
         assert _gemm(**bad) == nc.NC_ESHAPE, bad
     for bad in (dict(A=24), dict(B=8), dict(D=24), dict(sa=18), dict(sb=17), dict(lda=264), dict(ldb=257), dict(ldd=68),
                 dict(epi=nc.NC_EPI_STORE_F32, ldd=66), dict(epi=nc.NC_EPI_RELU2_FP8, ldd=72),
