@@ -115,6 +115,7 @@ __device__ __forceinline__ float max16(float a) {
 // x' = x + res (rounded to T);  r = 1/sqrt(mean(x'^2) + eps);  y = r x' held in
 // e4m3 by blocks: since y / max|y| = x' / max|x'|, the codes come from x'
 // alone and only the scale, r max|x'| / 448, carries the norm.
+// Bandwidth-bound: 32,768 x 1280 bf16 rows 48 us, 6.1 TB/s; one row 3.4 us.
 // WPR warps per row (one where there are rows enough to fill the SMs, four
 // otherwise): the row is read once and stays in registers, in its storage type
 // until it is used, so that all of its loads are in flight.
@@ -221,6 +222,8 @@ __global__ void __launch_bounds__(256) add_rmsnorm_fp8_kernel(const T *x, const 
 // 1 x 128 blocks: a warp takes 256 columns of four rows, 16 lanes to a block,
 // a CTA 32 rows of the same columns.  Lanes 0..3 and 16..19 then hold one
 // row's maximum each, so the four rows' scales take one division and one store.
+// 16,384 x 2048 bf16: 24 us, 4.2 TB/s: a CTA's loads, its arithmetic and its
+// stores follow one another, and no more CTAs fit an SM's registers.
 // (Measured against CTAs that walk several units with the next one's loads in
 // flight: 23.9 against 26.8 us at 16,384 x 2048 bf16.)
 template <typename T>
@@ -252,6 +255,8 @@ __global__ void __launch_bounds__(256) quant_rows_kernel(const T *__restrict__ x
 
 // 128 x 128 blocks: one CTA per block, held in registers as loaded between the
 // reduction and the codes (16 lanes across, 32 rows per pass, 4 passes).
+// 8192 x 2048 fp32: 20 us, 4.2 TB/s; the block's maximum stands between its
+// loads and its stores, and two or three CTAs per SM hide that in part.
 template <typename T>
 __global__ void __launch_bounds__(512, sizeof(T) == 2 ? 3 : 2)
     quant_tiles_kernel(const T *__restrict__ x, int64_t ldx, uint8_t *__restrict__ q, int64_t ldq,

@@ -206,6 +206,8 @@ int nc_rope_qknorm_bwd(const nc_model *m, void *dqkv, const void *qkv, int64_t l
  * 128 x 128 blocks, s[nb * lds + kb], lds >= ceil(cols / 128).  A last block
  * shorter than 128 has a scale of its own.  These calls run forward only:
  * the 8-bit copies serve, the weights that train stay in the model dtype.
+ * They need no workspace and can be captured into graphs; the first call of
+ * nc_gemm_fp8 in a context sets its kernels up: make it before a capture.
  *
  * The residual's addition, RMSNorm and the 8-bit operand of the projection
  * that follows, in one pass:
