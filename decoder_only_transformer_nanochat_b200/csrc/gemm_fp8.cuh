@@ -126,9 +126,9 @@ __device__ __forceinline__ float softcap8(float z) {
 // for them in its shared memory; after one cluster barrier it adds them in
 // rank order (the bits do not depend on which CTA ends first) and stores.
 //
-// Measured: one row x 1536 x 1280 6.1 us in a graph (launch, set-up, one load and
+// Measured: one row x 1536 x 1280 4.8 us in a graph (launch, set-up, one load and
 // one cluster barrier; the weights alone would take 0.3); 16 rows x 65,536 x
-// 1280 20.8 us, 4.1 TB/s.  The sums are 4-byte stores to the owner because a
+// 1280 17.7 us in a row of calls, 4.9 TB/s.  The sums are 4-byte stores to the owner because a
 // pull needs a second cluster barrier (one row 6.5 us, pushed 5.4).
 //
 // kMany: more tiles than two CTAs per SM hold at once (the logits of a few
@@ -291,6 +291,7 @@ __global__ void __launch_bounds__(RowsCfg<TN, kMany>::kThreads, RowsCfg<TN, kMan
       *abort_flag = 0;
       asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
       // the ring's first loads need nothing that the other warps set up
+      fp8::pdl_wait();
       for (int s = 0; s < min(S, kb1 - kb0); ++s) {
         const uint32_t sw = smem_u32(smem + s * Cfg::kStageBytes);
         mbar_expect_tx(full_bar(s), Cfg::kStageBytes);
@@ -305,6 +306,8 @@ __global__ void __launch_bounds__(RowsCfg<TN, kMany>::kThreads, RowsCfg<TN, kMan
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
+  fp8::pdl_start();  // only now: a successor's CTA that waits for this grid must not hold the TMEM that this one needs
+  fp8::pdl_wait();
 
   if (warp == 0) {
     // ---------------- TMA producer ----------------
@@ -652,6 +655,8 @@ __global__ void __launch_bounds__(PTHREADS, 1)
   cluster_sync_all();  // both CTAs' barriers exist before any cross-CTA signal
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
+  fp8::pdl_start();  // only now: a successor's CTA that waits for this grid must not hold the TMEM that this one needs
+  fp8::pdl_wait();
 
   if (warp < 4) {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(PREGS_LOW));
@@ -1033,19 +1038,8 @@ inline cudaError_t launch_rows(const GemmFp8Problem &g, int num_sms, int *status
   p.splits = 1;
   while (!kMany && p.splits < 8 && 2 * p.splits <= p.kblocks && tiles * 2 * p.splits <= Cfg::kCtas * num_sms) p.splits *= 2;
   if (tiles * p.splits > INT32_MAX) return cudaErrorInvalidValue;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(tiles * p.splits));
-  cfg.blockDim = dim3(Cfg::kThreads);
-  cfg.dynamicSmemBytes = Cfg::kSmem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = p.splits;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = p.splits > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, gemm_fp8_rows_kernel<TN, kMany>, mw, mx, p);
+  return fp8::launch(gemm_fp8_rows_kernel<TN, kMany>, (unsigned)(tiles * p.splits), Cfg::kThreads, Cfg::kSmem, p.splits, st, mw,
+                     mx, p);
 }
 
 inline cudaError_t launch_pair(const GemmFp8Problem &g, int num_sms, int *status, cudaStream_t st) {
@@ -1083,25 +1077,17 @@ inline cudaError_t launch_pair(const GemmFp8Problem &g, int num_sms, int *status
   // to each it pays (512 x 1536 x 6144: 31.1 us whole, 19.6 us in four; 1024 x
   // 1280 x 1280: 12.0 us whole, 14.9 us in two).
   while (p.splits < PSPLITS && p.kblocks >= 24 * p.splits && p.units * 2 * p.splits <= num_sms / 2) p.splits *= 2;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * p.splits * min(p.units, num_sms / 2));
-  cfg.blockDim = dim3(PTHREADS);
-  cfg.dynamicSmemBytes = PSMEM;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2 * p.splits;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  auto go = [&](auto *kernel) {
+    return fp8::launch(kernel, (unsigned)(2 * p.splits * std::min(p.units, num_sms / 2)), PTHREADS, PSMEM, 2 * p.splits, st, ma,
+                       mb, md, p);
+  };
   switch (g.epi) {
-    case EPI_STORE: return cudaLaunchKernelEx(&cfg, gemm_fp8_pair_kernel<EPI_STORE>, ma, mb, md, p);
-    case EPI_STORE_F32: return cudaLaunchKernelEx(&cfg, gemm_fp8_pair_kernel<EPI_STORE_F32>, ma, mb, md, p);
-    case EPI_ADD: return cudaLaunchKernelEx(&cfg, gemm_fp8_pair_kernel<EPI_ADD>, ma, mb, md, p);
-    case EPI_RELU2: return cudaLaunchKernelEx(&cfg, gemm_fp8_pair_kernel<EPI_RELU2>, ma, mb, md, p);
-    case EPI_SOFTCAP: return cudaLaunchKernelEx(&cfg, gemm_fp8_pair_kernel<EPI_SOFTCAP>, ma, mb, md, p);
-    default: return cudaLaunchKernelEx(&cfg, gemm_fp8_pair_kernel<EPI_RELU2_FP8>, ma, mb, md, p);
+    case EPI_STORE: return go(gemm_fp8_pair_kernel<EPI_STORE>);
+    case EPI_STORE_F32: return go(gemm_fp8_pair_kernel<EPI_STORE_F32>);
+    case EPI_ADD: return go(gemm_fp8_pair_kernel<EPI_ADD>);
+    case EPI_RELU2: return go(gemm_fp8_pair_kernel<EPI_RELU2>);
+    case EPI_SOFTCAP: return go(gemm_fp8_pair_kernel<EPI_SOFTCAP>);
+    default: return go(gemm_fp8_pair_kernel<EPI_RELU2_FP8>);
   }
 }
 

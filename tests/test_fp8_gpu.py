@@ -622,6 +622,63 @@ def test_mlp_of_a_block(nc, M):
     assert (np.abs(_host(b["xo"]) - ref) <= 1.01 * ex + 2.0 ** -8 * (np.abs(ref) + ex)).all()
 
 
+@pytest.mark.parametrize("M", [3, 150, 700])
+def test_chain_of_calls_without_waiting(nc, M):
+    """Forty MLPs in a row on the same stream buffers, each call's operands the last one's results: the bits are
+    those of the same calls waited for one by one (a call that reads before the one ahead of it has written, or
+    writes what that one still reads, shows), eager and replayed from a graph."""
+    import torch
+    C, F, n = 256, 1024, 40
+    t, _ = _mlp_inputs(M, C, F)
+    b = _mlp_buffers(M, C, F)
+    _mlp_weights(nc, t, b, C, F, _stream())
+    x0 = t[0].clone()
+
+    def step(wait):
+        # x += xo and its norm's codes feed the products (unnormalised, relu^2 would square x at every step: no finite
+        # chain); the quantiser before writes the same codes' place, for the norm to write over
+        st = _stream()
+        calls = [
+            lambda: nc.nc_quant_fp8(t[0].data_ptr(), C, b["q"].data_ptr(), C, b["s"].data_ptr(), M, M, C, 1, nc.NC_BF16, st),
+            lambda: nc.nc_add_rmsnorm_fp8(t[0].data_ptr(), b["xo"].data_ptr(), t[0].data_ptr(), b["q"].data_ptr(),
+                                          b["s"].data_ptr(), M, None, M, C, nc.NC_BF16, st),
+            lambda: nc.nc_gemm_fp8(b["q"].data_ptr(), C, b["s"].data_ptr(), M, b["w1"].data_ptr(), C, b["s1"].data_ptr(),
+                                   _blocks(C), b["h"].data_ptr(), F, b["sh"].data_ptr(), M, M, F, C, nc.NC_EPI_RELU2_FP8, st),
+            lambda: nc.nc_gemm_fp8(b["h"].data_ptr(), F, b["sh"].data_ptr(), M, b["w2"].data_ptr(), F, b["s2"].data_ptr(),
+                                   _blocks(F), b["xo"].data_ptr(), C, None, 0, M, C, F, nc.NC_EPI_STORE, st)]
+        for c in calls:
+            assert c() == 0
+            if wait:
+                torch.cuda.synchronize()
+        t[0].mul_(0.5)  # another kind of kernel between
+        if wait:
+            torch.cuda.synchronize()
+
+    def run(wait):
+        t[0].copy_(x0)
+        b["xo"].zero_()
+        for _ in range(n):
+            step(wait)
+        torch.cuda.synchronize()
+        return t[0].clone(), b["q"].view(torch.uint8).clone(), b["h"].view(torch.uint8).clone()
+    want = run(True)
+    assert torch.isfinite(want[0].float()).all() and (want[0] != 0).any()
+    for _ in range(3):
+        for w, g in zip(want, run(False)):
+            assert torch.equal(w, g)
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        for _ in range(n):
+            step(False)
+    t[0].copy_(x0)
+    b["xo"].zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(t[0], want[0]) and torch.equal(b["h"].view(torch.uint8), want[2])
+    assert nc.nc_ops_status(_stream(), 60000) == 0
+
+
 def test_mlp_on_streams_and_in_graphs(nc):
     """The same run on a side stream, and captured twice into graphs whose replays overlap on two streams with
     buffers of their own: bit for bit the eager result on the default stream."""
