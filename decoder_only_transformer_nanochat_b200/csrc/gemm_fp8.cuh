@@ -477,9 +477,9 @@ __global__ void __launch_bounds__(RowsCfg<TN, kMany>::kThreads, RowsCfg<TN, kMan
 // A thread's 128 columns are also one 1 x 128 output block, so the 8-bit
 // epilogue finds its maximum without leaving the thread.
 //
-// What bounds it: an accumulator's way round.  A K block takes about 820 cycles
-// where its MMAs take 512 (16384 x 2048 x 8192 with the residual add: 257 us,
-// 2.14 PFLOP/s; 32768 x 5120 x 1280 with relu^2 to 8 bits: 227 us, 1.89); the
+// What bounds it: an accumulator's way round.  A K block takes about 780 cycles
+// where its MMAs take 512 (16384 x 2048 x 8192 with the residual add: 246 us,
+// 2.23 PFLOP/s; 32768 x 5120 x 1280 with relu^2 to 8 bits: 217 us, 1.98); the
 // loop without sums, one hand-over a tile, runs at 180 us and 3.06 PFLOP/s.
 // Two accumulators are all that TMEM holds at this tile, and a smaller tile
 // moves more operand bytes per product.  Handing over whole accumulators
@@ -750,15 +750,16 @@ __global__ void __launch_bounds__(PTHREADS, 1)
     uint32_t phase = 0;
     bool ok = true;
     const uint32_t tempty0 = cluster_addr(tempty_bar(cg), lead);
-    // This thread's two scales of K blocks kb and kb + 1, fetched as one pair
-    // while the pair before is used (a wait for the older of two outstanding
-    // loads would be one for the newer too).  Rows and columns outside the
-    // matrix take the scales of the last one inside; they are not stored.
-    float fa[2], fb[2];
+    // This thread's two scales of AHEAD K blocks, fetched together while those
+    // of the AHEAD before are used (a wait for the older of outstanding loads
+    // would be one for the newer too).  Rows and columns outside the matrix
+    // take the scales of the last one inside; they are not stored.
+    constexpr int AHEAD = 5;  // us at 16384 x 2048 x 8192: 2 262, 3 252, 4 248, 5 246, 6 262 (registers spill)
+    float fa[AHEAD], fb[AHEAD];
     const float *pa = nullptr, *pb = nullptr;
     auto fetch = [&](int kb) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < AHEAD; ++i) {
         const int k = min(kb + i, kb1 - 1);
         fa[i] = pa[k * p.lsa];
         fb[i] = pb[k];
@@ -794,8 +795,7 @@ __global__ void __launch_bounds__(PTHREADS, 1)
       uint64_t sum[64];
 #pragma unroll
       for (int i = 0; i < 64; ++i) sum[i] = 0;
-      // Two 32-column loads are in flight while the two before are summed; the
-      // next K block's first two are requested before this block's last sums.
+      // Two 32-column loads are in flight at a time.
       uint32_t v0[32], v1[32];
       auto add = [&](uint32_t (&v)[32], int c, uint64_t f) {
 #pragma unroll
@@ -807,14 +807,16 @@ __global__ void __launch_bounds__(PTHREADS, 1)
         tmem_ld32_nw(t_row + acc * 256, v0);
         tmem_ld32_nw(t_row + acc * 256 + 32, v1);
       }
-      for (int kp = kb0; kp < kb1 && ok; kp += 2) {
-        const float s2[2] = {fa[0] * fb[0], fa[1] * fb[1]};
-        if (kp + 2 < kb1) fetch(kp + 2);
+      for (int kp = kb0; kp < kb1 && ok; kp += AHEAD) {
+        float sc[AHEAD];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < AHEAD; ++i) sc[i] = fa[i] * fb[i];
+        if (kp + AHEAD < kb1) fetch(kp + AHEAD);
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
           const int kb = kp + i;
           if (kb >= kb1) break;
-          const uint64_t f = f2(s2[i], s2[i]);
+          const uint64_t f = f2(sc[i], sc[i]);
           tmem_wait32(v0, v1);
           add(v0, 0, f);
           tmem_ld32_nw(t_row + acc * 256 + 64, v0);
@@ -826,15 +828,16 @@ __global__ void __launch_bounds__(PTHREADS, 1)
           if (lane == 0) mbar_arrive_relaxed(tempty0 + acc * 16);
           acc ^= 1;
           if (++stage == S) { stage = 0; phase ^= 1; }
+          // the rest of this block's work comes before the next one is looked
+          // for: what lies between that and its hand-back is the way round
           add(v0, 2, f);
-          const bool more = kb + 1 < kb1;
-          if (more) {
+          add(v1, 3, f);
+          if (kb + 1 < kb1) {
             ok = wait_done();
             if (!ok) break;
             tmem_ld32_nw(t_row + acc * 256, v0);
+            tmem_ld32_nw(t_row + acc * 256 + 32, v1);
           }
-          add(v1, 3, f);
-          if (more) tmem_ld32_nw(t_row + acc * 256 + 32, v1);
         }
       }
       if (u + n_clusters < p.units) first_scales(u + n_clusters);
