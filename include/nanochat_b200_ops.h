@@ -208,6 +208,9 @@ int nc_rope_qknorm_bwd(const nc_model *m, void *dqkv, const void *qkv, int64_t l
  * the 8-bit copies serve, the weights that train stay in the model dtype.
  * They need no workspace and can be captured into graphs; the first call of
  * nc_gemm_fp8 in a context sets its kernels up: make it before a capture.
+ * Their launches overlap the end of the kernel before them in the stream
+ * (programmatic stream serialization); they touch memory only once that kernel
+ * has completed, so the order of the stream's effects is what it always is.
  *
  * The residual's addition, RMSNorm and the 8-bit operand of the projection
  * that follows, in one pass:
