@@ -114,7 +114,7 @@ __device__ __forceinline__ float softcap8(float z) {
 }
 
 // ===========================================================================
-// Few rows: the weights are the M = 128 operand of the tensor core and TN
+// Few rows (or few tiles): the weights are the M = 128 operand of the tensor core and TN
 // activation rows the N operand, so one decoded token costs an N = 16 tile
 // instead of a 128-row one.
 //
@@ -1025,6 +1025,11 @@ inline bool make_map8(CUtensorMap *map, const void *base, int64_t rows, int64_t 
 
 inline Out out_of(const GemmFp8Problem &g) { return Out{g.M, g.N, g.D, g.ldd, g.sd, g.lsd}; }
 
+// SMs that clusters of four or eight CTAs can fill at once, one CTA on each: a
+// cluster stays within one of the groups of SMs that the GPU is made of (36 clusters of
+// four on 148 SMs ran in two turns, 32 in one).
+inline int cluster_room(int num_sms) { return num_sms * 7 / 8; }
+
 template <int TN, bool kMany>
 inline cudaError_t launch_rows(const GemmFp8Problem &g, int num_sms, int *status, cudaStream_t st) {
   using Cfg = RowsCfg<TN, kMany>;
@@ -1039,7 +1044,9 @@ inline cudaError_t launch_rows(const GemmFp8Problem &g, int num_sms, int *status
   const int64_t tiles = (int64_t)p.n_m * ((g.N + 127) / 128);
   // cut K while every CTA still finds a place at once and keeps a K block
   p.splits = 1;
-  while (!kMany && p.splits < 8 && 2 * p.splits <= p.kblocks && tiles * 2 * p.splits <= Cfg::kCtas * num_sms) p.splits *= 2;
+  while (!kMany && p.splits < 8 && 2 * p.splits <= p.kblocks &&
+         tiles * 2 * p.splits <= Cfg::kCtas * (p.splits > 1 ? cluster_room(num_sms) : num_sms))
+    p.splits *= 2;
   if (tiles * p.splits > INT32_MAX) return cudaErrorInvalidValue;
   return fp8::launch(gemm_fp8_rows_kernel<TN, kMany>, (unsigned)(tiles * p.splits), Cfg::kThreads, Cfg::kSmem, p.splits, st, mw,
                      mx, p);
@@ -1122,12 +1129,14 @@ inline cudaError_t init() {
 }  // namespace tc8
 
 inline cudaError_t launch_gemm_fp8(const GemmFp8Problem &g, int num_sms, int *status, cudaStream_t st) {
-  // 256-row tiles from 257 rows on, and from 65 on where 128-row tiles leave no
-  // room to cut K (256 x 5120 x 1280: 12.2 us against 17.1; 96 x 1280 x 5120: 16.9
-  // against 12.7 with 128-row tiles)
-  const int64_t across = ((int64_t)g.N + 127) / 128;
-  if (g.M > 256 || (g.M > 64 && 2 * across * ((g.M + 127) / 128) > num_sms))
-    return tc8::launch_pair(g, num_sms, status, st);
+  // 128-row tiles where K can be cut over four CTAs that all run at once (300 x
+  // 1280 x 5120: 13.8 us against 17.4 with 256-row tiles, 4000 x 128 x 4096: 13.3
+  // against 15.8; with two K blocks, 3643 x 101 x 144, 10.4 against 8.1), up to
+  // 256 rows where it can over two (96 x 1280 x 5120: 12.7 against 16.9; 256 x
+  // 5120 x 1280, where it cannot: 17.1 against 12.2).  256-row tiles otherwise.
+  const int64_t across = ((int64_t)g.N + 127) / 128, tiles = across * ((g.M + 127) / 128);
+  const bool few = 4 * tiles <= tc8::cluster_room(num_sms) && g.K > 7 * tc8::BK;
+  if (g.M > 64 && !few && (g.M > 256 || 2 * tiles > num_sms)) return tc8::launch_pair(g, num_sms, status, st);
   // the logits of a few rows (16 x 65,536 x 1280: 21.2 us with four CTAs per SM, 24.9 with two)
   if (g.M <= 16 && across > 2 * num_sms) return tc8::launch_rows<16, true>(g, num_sms, status, st);
   if (g.M <= 16) return tc8::launch_rows<16, false>(g, num_sms, status, st);

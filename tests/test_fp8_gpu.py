@@ -351,6 +351,7 @@ SHAPES = [
     (200, 1003, 656), (300, 520, 1040), (515, 776, 1296), (1030, 264, 272), (270, 200, 8208),
     (20485, 392, 272),     # several tiles per pair of CTAs, the last column half of 8 columns
     (300, 1003, 272), (290, 5, 144), (513, 385, 130), (300, 262, 16),   # N that no 16-byte unit divides
+    (1000, 500, 1100), (4000, 128, 1040), (300, 1280, 1296), (260, 4608, 1040),   # 128-row tiles with K cut, and not
     (100, 10241, 400), (256, 9600, 272),   # 256-row tiles for fewer rows
     (270, 300, 3200), (400, 1003, 6416),   # K cut over two and four pairs of CTAs
     (40, 20485, 144),      # many weight tiles
