@@ -127,6 +127,43 @@ template <> __device__ __forceinline__ uint2 quant8<float>(const float (&v)[8], 
   return make_uint2(cvt4(y[0], y[1], y[2], y[3]), cvt4(y[4], y[5], y[6], y[7]));
 }
 
+// The codes of fp32 values that stand in f32x2 pairs, as an epilogue has them,
+// by the same rule, RN_e4m3(RN(RN(448 v) / a)), without a division or a branch
+// per value: n = RN(448 v), y = RN(n / a) up to 1.5 units, and one step with
+// the residual, RN(y + (n - y a) / a), from the rounded reciprocal of a
+// (Markstein, "Computation of elementary functions on the IBM RISC System/6000
+// processor").  Where y is within a unit, which holds for n >= a in
+// significands, that is the quotient rounded to nearest; elsewhere it is off
+// by less than 2^-47 before its rounding, and n / a, as a quotient of 24-bit
+// numbers beside a border of 5 bits, stays that far from the middle between two
+// floats unless a's 24-bit significand is within 5 of a multiple of 2^20.  All
+// of those (and 40 to each side) give the right code for every border and
+// every n around it.  v and a are scaled by one power of two, exactly, so that
+// a is in [1, 4) (or, for a < 2^-119, at least 2^-30): nothing overflows, and no
+// residual of a value that gets a code but 0 is subnormal.  Against one product
+// with an approximate 448 / a this costs 15 us of 230 at 32,768 x 5120 x 1280
+// (two codes of bracketing products compared, the residual step only where they differ: 12 us).
+struct Ratio {
+  uint64_t k, ra, na;  // 448 and a scaled: n = k v; 1 / a; -a
+  __device__ __forceinline__ explicit Ratio(float a) {
+    const int e = min(max((int)(__float_as_uint(a) >> 23), 8), 253);  // exponent field
+    const float s = __uint_as_float((uint32_t)(254 - e) << 23), kf = kMax * s;
+    const bool any = a > 0.f && a < INFINITY;  // else codes are 0, but for what is not finite
+    const float af = any ? a * s : 1.f, r = any ? __frcp_rn(af) : 0.f;
+    k = f2(kf, kf);
+    ra = f2(r, r);
+    na = f2(-af, -af);
+  }
+  __device__ __forceinline__ uint32_t codes4(uint64_t v0, uint64_t v1) const {
+    const uint64_t n0 = mul2(v0, k), n1 = mul2(v1, k);
+    const uint64_t y0 = mul2(n0, ra), y1 = mul2(n1, ra);
+    float a, b, c, d;
+    f2split(fma2(fma2(y0, na, n0), ra, y0), a, b);
+    f2split(fma2(fma2(y1, na, n1), ra, y1), c, d);
+    return cvt4(a, b, c, d);
+  }
+};
+
 __device__ __forceinline__ float amax8(const float (&v)[8]) {
   float a = 0.f;
 #pragma unroll

@@ -201,9 +201,7 @@ __device__ __forceinline__ void store_block_row(const Out &p, int epi, int m, in
     for (int j = 0; j < 4; ++j)
       if (j < left) a = fmaxf(a, v[j]);
     a = warp_max(a);
-    const fp8::Quant z(a);
-    const float f = z.inv, pre = z.pre;
-    const uint32_t c = fp8::cvt4(v[0] * pre * f, v[1] * pre * f, v[2] * pre * f, v[3] * pre * f);
+    const uint32_t c = fp8::Ratio(a).codes4(f2(v[0], v[1]), f2(v[2], v[3]));
     uint8_t *d = reinterpret_cast<uint8_t *>(p.D) + (int64_t)m * p.ldd + n;
     if (left >= 4) *reinterpret_cast<uint32_t *>(d) = c;
     else
@@ -907,23 +905,12 @@ __global__ void __launch_bounds__(PTHREADS, 1)
           f2split(sum[i], lo, hi);
           a = max3(a, lo, hi);
         }
-        const fp8::Quant z(a);
-        const uint64_t f = f2(z.inv, z.inv);
-        if (__any_sync(0xffffffffu, z.pre != 1.f)) {  // a tiny row is scaled up first
-          const uint64_t pre = f2(z.pre, z.pre);
-#pragma unroll
-          for (int i = 0; i < 64; ++i) sum[i] = mul2(sum[i], pre);
-        }
+        const fp8::Ratio z(a);
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
           uint32_t w[4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            float o[4];
-            f2split(mul2(sum[8 * q + 2 * j], f), o[0], o[1]);
-            f2split(mul2(sum[8 * q + 2 * j + 1], f), o[2], o[3]);
-            w[j] = fp8::cvt4(o[0], o[1], o[2], o[3]);
-          }
+          for (int j = 0; j < 4; ++j) w[j] = z.codes4(sum[8 * q + 2 * j], sum[8 * q + 2 * j + 1]);
           *reinterpret_cast<uint4 *>(my + ((q ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
         }
         pair_tail<false, uint8_t>(p, my, lane, mw + lane, n0, 128);

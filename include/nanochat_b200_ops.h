@@ -235,7 +235,8 @@ int nc_quant_fp8(const void *x, int64_t ldx, void *q, int64_t ldq, float *s, int
                  int block_rows, int dtype, void *stream);
 
 /* relu(acc)^2 left in 8 bits by 1 x 128 blocks, the A operand of the next
- * product (nc_gemm_fp8 only) */
+ * product (nc_gemm_fp8 only): the codes and scales that nc_quant_fp8 gives for
+ * the same call's fp32 sums (NC_EPI_STORE_F32), their positive parts squared */
 #define NC_EPI_RELU2_FP8 7
 
 /* Product of 8-bit operands:
