@@ -246,6 +246,9 @@ int nc_quant_fp8(const void *x, int64_t ldx, void *q, int64_t ldq, float *s, int
  * scales (y = x W^T).  Each block of K is summed on the tensor cores and the
  * scaled blocks in fp32, in an order that depends on the shape alone: the
  * same call gives the same bits.
+ * The product of a block's two scales is formed first, in fp32: all bits of the
+ * result are there while it is 0 or at least 2^-126, it has steps of 2^-149
+ * below that, and from 2^128 on the block's sums come out infinite or NaN.
  * epilogue: NC_EPI_STORE, _ADD (D += acc), _RELU2 or _SOFTCAP with D bf16,
  * NC_EPI_STORE_F32 with D fp32, or NC_EPI_RELU2_FP8 with D e4m3 and its scales
  * in sd[(n/128)*lsd + m]; sd and lsd are not looked at otherwise.  Others:
