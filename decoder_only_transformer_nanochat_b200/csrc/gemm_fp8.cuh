@@ -107,10 +107,14 @@ __device__ __forceinline__ float relu_nan(float x) {
   return y;
 }
 
-// 15 tanh(z / 15) from one exponential: t = (1 - E) / (1 + E), E = exp(-2 |z| / 15)
+// 15 tanh(z / 15) to 2^-15 of its value: t = (1 - E) / (1 + E), E = exp(-2 |z| / 15),
+// off by the error of E, up to 2^-22, against 1 - E; z itself up to |z| = 0.09,
+// where tanh's next term is 2^-16.3 and 1 - E has fallen to 2^-6.4.  (tanh's
+// series to 2^-21 below 15 / 4 instead: 265 us against 238 at 2048 x 65,536 x 1280.)
 __device__ __forceinline__ float softcap8(float z) {
   const float e = __expf(-2.f / kSoftcap * fabsf(z));
-  return copysignf(kSoftcap * __fdividef(1.f - e, 1.f + e), z);
+  const float t = copysignf(kSoftcap * __fdividef(1.f - e, 1.f + e), z);
+  return fabsf(z) < 0.09f ? z : t;
 }
 
 // ===========================================================================

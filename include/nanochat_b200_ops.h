@@ -253,6 +253,8 @@ int nc_quant_fp8(const void *x, int64_t ldx, void *q, int64_t ldq, float *s, int
  * NC_EPI_STORE_F32 with D fp32, or NC_EPI_RELU2_FP8 with D e4m3 and its scales
  * in sd[(n/128)*lsd + m]; sd and lsd are not looked at otherwise.  Others:
  * NC_EINVAL.
+ * The softcap is right to 2^-15 of its value, down to the smallest, before the
+ * rounding to bf16.
  * 1 <= M, N, K <= 2^30, lda, ldb >= K, ldd >= N (each below 2^38), lsa (and
  * lsd) >= M, lsb >= ceil(K / 128), else NC_ESHAPE; A, B, D 16-byte aligned with 16-byte
  * row strides, the scales 4-byte aligned, else NC_EALIGN.  D and sd must not
