@@ -31,6 +31,9 @@ constexpr int kBlock = 128;     // values per scale along a row
 // completed and its writes are visible.  Launch and set-up then overlap the
 // predecessor's end (calls in a row, us: 16 x 65,536 x 1280 GEMM 20.5 -> 17.7,
 // 1001 x 1003 x 1040 14.3 -> 12.7, an 8192 x 2048 weight's codes 20.3 -> 17.7).
+// So what the kernel before may have written is not read-only while these run:
+// inputs carry no const __restrict__, under which a load could be taken through
+// the read-only path or moved above the wait.
 __device__ __forceinline__ void pdl_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
@@ -295,7 +298,7 @@ __global__ void __launch_bounds__(256) add_rmsnorm_fp8_kernel(const T *x, const 
 // (Measured against CTAs that walk several units with the next one's loads in
 // flight: 23.9 against 26.8 us at 16,384 x 2048 bf16.)
 template <typename T>
-__global__ void __launch_bounds__(256) quant_rows_kernel(const T *__restrict__ x, int64_t ldx, uint8_t *__restrict__ q,
+__global__ void __launch_bounds__(256) quant_rows_kernel(const T *x, int64_t ldx, uint8_t *__restrict__ q,
                                                          int64_t ldq, float *__restrict__ s, int64_t lds, int rows,
                                                          int cols, unsigned segs) {
   pdl_start();
@@ -329,7 +332,7 @@ __global__ void __launch_bounds__(256) quant_rows_kernel(const T *__restrict__ x
 // loads and its stores, and two or three CTAs per SM hide that in part.
 template <typename T>
 __global__ void __launch_bounds__(512, sizeof(T) == 2 ? 3 : 2)
-    quant_tiles_kernel(const T *__restrict__ x, int64_t ldx, uint8_t *__restrict__ q, int64_t ldq,
+    quant_tiles_kernel(const T *x, int64_t ldx, uint8_t *__restrict__ q, int64_t ldq,
                        float *__restrict__ s, int64_t lds, int rows, int cols, unsigned kbs) {
   __shared__ float sh[16];
   pdl_start();
