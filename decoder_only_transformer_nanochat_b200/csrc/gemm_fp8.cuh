@@ -12,6 +12,7 @@
 #pragma once
 
 #include "fp8.cuh"
+#include "fp8_plan.h"
 #include "gemm_tc.cuh"
 
 namespace nc {
@@ -143,7 +144,7 @@ template <int TN, bool kMany> struct RowsCfg {
   static constexpr int kCols = TN * 4 / kEpiWarps;         // activation rows per thread
   static constexpr int kThreads = 64 + 32 * kEpiWarps;
   static constexpr int kStageBytes = (128 + TN) * BK;
-  static constexpr int kCtas = kMany ? 4 : TN > 64 ? 1 : 2;  // per SM
+  static constexpr int kCtas = rows_ctas(TN, kMany);       // per SM
   static constexpr int kStages = kMany ? 3 : TN == 16 ? 5 : TN == 64 ? 3 : 4;
   static constexpr int kAccs = 4;                          // TMEM accumulators in flight
   static constexpr int kTmemCols = kAccs * TN;             // 64, 128, 256, 512: a power of two
@@ -504,7 +505,7 @@ constexpr int PEPI_WARPS = 8;
 constexpr int PTHREADS = 128 + 32 * PEPI_WARPS;
 constexpr int PREGS = 168, PREGS_LOW = 24, PREGS_HIGH = 240;
 static_assert(128 * PREGS_LOW + 32 * PEPI_WARPS * PREGS_HIGH <= PTHREADS * PREGS, "register split within the launch");
-constexpr int PSPLITS = 4;  // pairs per cluster at most: eight CTAs
+constexpr int PSPLITS = kMaxPairSplits;
 constexpr int PBOX = 32 * 128;
 constexpr int PSMEM = PSTAGES * PSTAGE_BYTES + PEPI_WARPS * 2 * PBOX + 256 + 1024;
 static_assert(PSMEM <= 232448, "shared memory per CTA");
@@ -513,25 +514,11 @@ static_assert(128 * 256 * 4 <= PSTAGES * PSTAGE_BYTES, "a split's sums fit the r
 // A TMA store writes whole 16-byte units of a row (measured: one byte per
 // element, N % 16 == 8, wrote eight bytes past N), so the map of D ends at the
 // last whole unit, column n_tma, and the threads take the rest of their row.
-// Division of numbers below 2^31 by a number known on the host, as a multiply
-// by its rounded-up reciprocal (Granlund and Montgomery, "Division by invariant
-// integers using multiplication"): every tile's epilogue waits for its place.
-struct ByHost {
-  uint32_t mul;
-  int shift;
-  __host__ explicit ByHost(uint32_t d = 1) {
-    shift = 31;
-    while ((1ull << (shift - 31)) < d) ++shift;
-    mul = (uint32_t)(((1ull << shift) + d - 1) / d);
-  }
-  __device__ __forceinline__ uint32_t div(uint32_t u) const { return (uint32_t)(((uint64_t)u * mul) >> shift); }
-};
-
 struct PairParams {
   Out out;
-  ByHost by_n, by_group;  // n_n, 16 n_n
+  PairTiles tiles;
   int kblocks, splits;  // pairs per cluster
-  int n_m, n_n, units, n_tma;
+  int units, n_tma;
   const float *sa, *sb;
   int64_t lsa, lsb;
   int *status;
@@ -581,20 +568,6 @@ __device__ __forceinline__ void mma8_pair(uint32_t d_tmem, uint64_t adesc, uint6
       "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
-}
-
-// Tiles in flight at once share operand panels in L2: with few N tiles those
-// of an M block are consecutive, with many 16 M blocks share each B panel.
-__device__ __forceinline__ void pair_tile(const PairParams &p, uint32_t u, int &m_blk, int &n_blk) {
-  if (p.n_n <= 16) {
-    m_blk = p.by_n.div(u);
-    n_blk = u - m_blk * p.n_n;
-    return;
-  }
-  const uint32_t g = p.by_group.div(u), r = u - g * 16 * p.n_n;
-  const int first = g * 16, size = min(p.n_m - first, 16);
-  n_blk = size == 16 ? r / 16 : r / size;
-  m_blk = first + r - n_blk * size;
 }
 
 template <int EPI>
@@ -670,7 +643,7 @@ __global__ void __launch_bounds__(PTHREADS, 1)
     bool ok = true;
     for (int u = cluster; u < p.units && ok; u += n_clusters) {
       int m_blk, n_blk;
-      pair_tile(p, u, m_blk, n_blk);
+      p.tiles.tile(u, m_blk, n_blk);
       const int m_row = m_blk * 256 + (int)rank * 128, n_row = n_blk * 256 + (int)rank * 64;
       for (int kb = kb0; kb < kb1; ++kb) {
         ok = __all_sync(0xffffffffu, wait8(done_bar(stage, 0), phase ^ 1, abort_flag, p.status) &&
@@ -769,7 +742,7 @@ __global__ void __launch_bounds__(PTHREADS, 1)
     };
     auto first_scales = [&](int u) {
       int m_blk, n_blk;
-      pair_tile(p, u, m_blk, n_blk);
+      p.tiles.tile(u, m_blk, n_blk);
       pa = p.sa + min(m_blk * 256 + (int)rank * 128 + quarter * 32 + lane, p.out.M - 1);
       pb = p.sb + (int64_t)min(n_blk * 2 + cg, (p.out.N - 1) >> 7) * p.lsb;
       fetch(kb0);
@@ -782,7 +755,7 @@ __global__ void __launch_bounds__(PTHREADS, 1)
     if (cluster < p.units) first_scales(cluster);
     for (int u = cluster; u < p.units; u += n_clusters) {
       int m_blk, n_blk;
-      pair_tile(p, u, m_blk, n_blk);
+      p.tiles.tile(u, m_blk, n_blk);
       const int mw = m_blk * 256 + (int)rank * 128 + quarter * 32;  // this warp's first row
       const int n0 = n_blk * 256 + cg * 128;
       const bool mine = mw < p.out.M && n0 < p.out.N;
@@ -959,7 +932,7 @@ __global__ void __launch_bounds__(PTHREADS, 1)
       // This CTA's part of its rows: one warp per row and 128-column block, the
       // pairs' sums added in order, four such rows' reads in flight.
       int m_blk, n_blk;
-      pair_tile(p, cluster, m_blk, n_blk);
+      p.tiles.tile(cluster, m_blk, n_blk);
       const int per = 128 / p.splits, first = m_blk * 256 + (int)rank * 128;
 #pragma unroll 1
       for (int i0 = (warp - 4) * 4; i0 < 2 * per && ok; i0 += 4 * PEPI_WARPS) {
@@ -1016,13 +989,8 @@ inline bool make_map8(CUtensorMap *map, const void *base, int64_t rows, int64_t 
 
 inline Out out_of(const GemmFp8Problem &g) { return Out{g.M, g.N, g.D, g.ldd, g.sd, g.lsd}; }
 
-// SMs that clusters of four or eight CTAs can fill at once, one CTA on each: a
-// cluster stays within one of the groups of SMs that the GPU is made of (36 clusters of
-// four on 148 SMs ran in two turns, 32 in one).
-inline int cluster_room(int num_sms) { return num_sms * 7 / 8; }
-
 template <int TN, bool kMany>
-inline cudaError_t launch_rows(const GemmFp8Problem &g, int num_sms, int *status, cudaStream_t st) {
+inline cudaError_t launch_rows(const GemmFp8Problem &g, const Plan &plan, int *status, cudaStream_t st) {
   using Cfg = RowsCfg<TN, kMany>;
   CUtensorMap mw, mx;
   if (!make_map8(&mw, g.B, g.N, g.K, g.ldb, 128) || !make_map8(&mx, g.A, g.M, g.K, g.lda, TN)) return cudaErrorInvalidValue;
@@ -1032,21 +1000,16 @@ inline cudaError_t launch_rows(const GemmFp8Problem &g, int num_sms, int *status
   p.n_m = (g.M + TN - 1) / TN;
   p.sa = g.sa; p.lsa = g.lsa; p.sb = g.sb; p.lsb = g.lsb;
   p.epi = g.epi; p.status = status;
-  const int64_t tiles = (int64_t)p.n_m * ((g.N + 127) / 128);
-  // cut K while every CTA still finds a place at once and keeps a K block
-  p.splits = 1;
-  while (!kMany && p.splits < 8 && 2 * p.splits <= p.kblocks &&
-         tiles * 2 * p.splits <= Cfg::kCtas * (p.splits > 1 ? cluster_room(num_sms) : num_sms))
-    p.splits *= 2;
-  if (tiles * p.splits > INT32_MAX) return cudaErrorInvalidValue;
-  return fp8::launch(gemm_fp8_rows_kernel<TN, kMany>, (unsigned)(tiles * p.splits), Cfg::kThreads, Cfg::kSmem, p.splits, st, mw,
+  p.splits = plan.splits;
+  if (plan.tiles * p.splits > INT32_MAX) return cudaErrorInvalidValue;
+  return fp8::launch(gemm_fp8_rows_kernel<TN, kMany>, (unsigned)(plan.tiles * p.splits), Cfg::kThreads, Cfg::kSmem, p.splits, st, mw,
                      mx, p);
 }
 
-inline cudaError_t launch_pair(const GemmFp8Problem &g, int num_sms, int *status, cudaStream_t st) {
+inline cudaError_t launch_pair(const GemmFp8Problem &g, const Plan &plan, int num_sms, int *status, cudaStream_t st) {
   CUtensorMap ma, mb, md;
   bool ok = make_map8(&ma, g.A, g.M, g.K, g.lda, 128) && make_map8(&mb, g.B, g.N, g.K, g.ldb, 64);
-  PairParams p;
+  PairParams p{out_of(g), PairTiles((g.M + 255) / 256, (g.N + 255) / 256)};
   const int unit = g.epi == EPI_RELU2_FP8 ? 16 : g.epi == EPI_STORE_F32 ? 4 : 8;  // values in 16 bytes
   p.n_tma = g.N / unit * unit;
   const int64_t cols = max(p.n_tma, unit);  // a D narrower than a unit leaves without the map
@@ -1062,22 +1025,12 @@ inline cudaError_t launch_pair(const GemmFp8Problem &g, int num_sms, int *status
     ok = ok && make_map(&md, g.D, g.M, cols, g.ldd, 64, 32);
   }
   if (!ok) return cudaErrorInvalidValue;
-  p.out = out_of(g);
+  if (plan.tiles > INT32_MAX / 2) return cudaErrorInvalidValue;  // unit + grid stays an int
   p.kblocks = (g.K + BK - 1) / BK;
-  p.n_m = (g.M + 255) / 256;
-  p.n_n = (g.N + 255) / 256;
-  if ((int64_t)p.n_m * p.n_n > INT32_MAX / 2) return cudaErrorInvalidValue;  // unit + grid stays an int
-  p.units = p.n_m * p.n_n;
-  p.by_n = ByHost(p.n_n);
-  p.by_group = ByHost(16u * p.n_n);
+  p.units = (int)plan.tiles;
+  p.splits = plan.splits;
   p.sa = g.sa; p.lsa = g.lsa; p.sb = g.sb; p.lsb = g.lsb;
   p.status = status;
-  p.splits = 1;
-  // A split costs about 6 us to exchange its sums (15 bytes a cycle and SM
-  // between shared memories), what ten K blocks take; with twelve blocks left
-  // to each it pays (512 x 1536 x 6144: 31.1 us whole, 19.6 us in four; 1024 x
-  // 1280 x 1280: 12.0 us whole, 14.9 us in two).
-  while (p.splits < PSPLITS && p.kblocks >= 24 * p.splits && p.units * 2 * p.splits <= num_sms / 2) p.splits *= 2;
   auto go = [&](auto *kernel) {
     return fp8::launch(kernel, (unsigned)(2 * p.splits * std::min(p.units, num_sms / 2)), PTHREADS, PSMEM, 2 * p.splits, st, ma,
                        mb, md, p);
@@ -1120,20 +1073,15 @@ inline cudaError_t init() {
 }  // namespace tc8
 
 inline cudaError_t launch_gemm_fp8(const GemmFp8Problem &g, int num_sms, int *status, cudaStream_t st) {
-  // 128-row tiles where K can be cut over four CTAs that all run at once (300 x
-  // 1280 x 5120: 13.8 us against 17.4 with 256-row tiles, 4000 x 128 x 4096: 13.3
-  // against 15.8; with two K blocks, 3643 x 101 x 144, 10.4 against 8.1), up to
-  // 256 rows where it can over two (96 x 1280 x 5120: 12.7 against 16.9; 256 x
-  // 5120 x 1280, where it cannot: 17.1 against 12.2).  256-row tiles otherwise.
-  const int64_t across = ((int64_t)g.N + 127) / 128, tiles = across * ((g.M + 127) / 128);
-  const bool few = 4 * tiles <= tc8::cluster_room(num_sms) && g.K > 7 * tc8::BK;
-  if (g.M > 64 && !few && (g.M > 256 || 2 * tiles > num_sms)) return tc8::launch_pair(g, num_sms, status, st);
-  // the logits of a few rows (16 x 65,536 x 1280: 21.2 us with four CTAs per SM, 24.9 with two)
-  if (g.M <= 16 && across > 2 * num_sms) return tc8::launch_rows<16, true>(g, num_sms, status, st);
-  if (g.M <= 16) return tc8::launch_rows<16, false>(g, num_sms, status, st);
-  if (g.M <= 32) return tc8::launch_rows<32, false>(g, num_sms, status, st);
-  if (g.M <= 64) return tc8::launch_rows<64, false>(g, num_sms, status, st);
-  return tc8::launch_rows<128, false>(g, num_sms, status, st);
+  const tc8::Plan p = tc8::plan(g.M, g.N, g.K, num_sms);
+  if (p.pair) return tc8::launch_pair(g, p, num_sms, status, st);
+  if (p.many) return tc8::launch_rows<16, true>(g, p, status, st);
+  switch (p.tn) {
+    case 16: return tc8::launch_rows<16, false>(g, p, status, st);
+    case 32: return tc8::launch_rows<32, false>(g, p, status, st);
+    case 64: return tc8::launch_rows<64, false>(g, p, status, st);
+    default: return tc8::launch_rows<128, false>(g, p, status, st);
+  }
 }
 
 }  // namespace nc
