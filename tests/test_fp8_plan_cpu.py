@@ -71,3 +71,22 @@ def test_division_by_reciprocal():
         us = {0, 1, d - 1, d, d + 1, 2 * d - 1, top, top - 1, top // d * d, top // d * d - 1} | {int(x) for x in r.randint(0, top, 50)}
         for u in us:
             assert lib().divided(u, d) == u // d, (u, d)
+
+
+def test_gpu_tests_reach_every_form():
+    """What the rule can choose (over a wide sample of sizes) is what the GPU tests' sizes make it choose."""
+    regimes = pytest.importorskip("test_fp8_regimes_gpu").REGIMES
+    for regime, sizes in regimes.items():
+        for s in sizes:
+            assert tuple(plan(*s)[:4]) == regime, (s, plan(*s))
+    r = np.random.RandomState(5)
+    seen = set()
+    for _ in range(40000):
+        seen.add(tuple(plan(*(int(np.exp(r.uniform(0, np.log(t)))) for t in (40000, 70000, 17000)))[:4]))
+    assert seen == set(regimes)
+    # tiles of pairs whose K is not cut: several a pair of CTAs, in whole and partial groups of 16, over a ragged second
+    # group of five K blocks
+    assert any(plan(M, N, K).tiles > 2 * 74 and N > 16 * 256 and M > 16 * 256 and -(-M // 256) % 16 and -(-K // 128) % 5
+               for M, N, K in regimes[(True, 0, False, 1)])
+    for M, C, F in ((300, 1504, 6416), (700, 1008, 5008)):  # the chain's down-projections
+        assert plan(M, C, F).pair and plan(M, C, F).splits > 1
