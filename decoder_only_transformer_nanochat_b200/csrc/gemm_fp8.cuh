@@ -58,12 +58,13 @@ __device__ __forceinline__ void mma8(uint32_t d_tmem, uint64_t adesc, uint64_t b
 }
 // Bounded wait for barriers that are handed over every K block: a count of
 // tries is the limit, which costs the callers one register where a clock would
-// cost several.  A try gives up after 2 us (measured), so 2^21 of them are
-// four seconds without progress.
-constexpr uint32_t kTries = 1u << 21;
-__device__ __forceinline__ bool wait8(uint32_t bar, uint32_t parity, volatile int *abort_flag, int *status) {
+// cost several.  A try gives up after 4 us (measured: 50,176 of them in 200 ms), so
+// 2^20 of them are four seconds without progress.
+constexpr uint32_t kTries = 1u << 20;
+__device__ __forceinline__ bool wait8(uint32_t bar, uint32_t parity, volatile int *abort_flag, int *status,
+                                      uint32_t tries = kTries) {
   for (uint32_t i = 1; !mbar_try(bar, parity); ++i) {
-    if ((i & 255) == 0 && (*abort_flag || i > kTries)) {
+    if ((i & 255) == 0 && (*abort_flag || i > tries)) {
       if (!*abort_flag) {
         *abort_flag = 1;
         set_status(status, kStatusTimeout);

@@ -670,22 +670,27 @@ inline bool attn_shape_ok(int B, int T, int H, int64_t ld) {
          (int64_t)B * T * ld <= ((int64_t)1 << 40);
 }
 
-// A bounded wait on an mbarrier that nothing completes: it runs out after
-// wait_ns and reports kStatusTimeout, the path every kernel wait takes when
-// its partner never arrives.
+// Bounded waits on an mbarrier that nothing completes, in the two forms that the
+// kernels use: limited by the clock (wait_ns), then by a count of tries (the
+// 8-bit GEMM's; a try takes about 4 us).  Each in turn gives up, and the
+// second reports kStatusTimeout, the path every kernel wait takes when its
+// partner never arrives; a third wait finds the abort flag and gives up at once.
 __global__ void wait_expiry_kernel(uint64_t wait_ns, int *status) {
   __shared__ __align__(8) uint64_t bar;
+  __shared__ int aborting, words[2];  // atomics reach shared memory, not a thread's own
   const uint32_t a = tc::smem_u32(&bar);
   tc::mbar_init(a, 1);
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  aborting = words[0] = words[1] = 0;
   const uint64_t t0 = tc::globaltimer();
   for (uint32_t i = 0;; ++i) {
     if (tc::mbar_try(a, 0)) return;  // never: nothing arrives on the barrier
-    if ((i & 63) == 0 && tc::globaltimer() - t0 > wait_ns) {
-      set_status(status, kStatusTimeout);
-      return;
-    }
+    if ((i & 63) == 0 && tc::globaltimer() - t0 > wait_ns) break;
   }
+  const bool counted = tc8::wait8(a, 0, &aborting, words, (uint32_t)(wait_ns / 4000));
+  const bool aborted = tc8::wait8(a, 0, &aborting, words + 1);
+  const volatile int *w = words;
+  if (!counted && w[0] == kStatusTimeout && !aborted && w[1] == 0) set_status(status, kStatusTimeout);
 }
 
 // ---------------------------------------------------------------------------

@@ -282,8 +282,10 @@ int nc_ops_status(void *stream, int timeout_ms);
 
 /* Self-check of the wait-expiry path: enqueues one thread that waits on a
  * barrier nothing completes, gives up after wait_us microseconds
- * (0 <= wait_us <= 1,000,000, else NC_EINVAL) and records a timeout in the op
- * status word, exactly as a kernel whose partner never arrives does.  The
+ * (0 <= wait_us <= 1,000,000, else NC_EINVAL), waits again with the limit that
+ * nc_gemm_fp8's waits have, a count of tries (about as long), and records a
+ * timeout in the op status word if both gave up and a further wait was given
+ * up at once for that, exactly as a kernel whose partner never arrives does.  The
  * next nc_ops_status then returns NC_ETIMEOUT.  No passage of the nanochat
  * pages corresponds to it; it lets a caller check that expired waits reach
  * the host without faulting or hanging the GPU. */
