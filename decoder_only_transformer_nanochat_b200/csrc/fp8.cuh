@@ -403,15 +403,19 @@ inline cudaError_t launch_add_rmsnorm(const T *x, const T *res, T *x_out, uint8_
              : launch_norm<T, false>(x, res, x_out, q, s, lds, r, M, C, st);
 }
 
+// CTAs of a quantiser's grid: 32 x 256 values each, or a block
+inline int64_t quant_units(int rows, int cols, int block_rows) {
+  const int across = block_rows == 1 ? 256 : 128, down = block_rows == 1 ? 32 : 128;
+  return ((int64_t)rows + down - 1) / down * ((cols + across - 1) / across);
+}
+
 template <typename T>
 inline cudaError_t launch_quant(const T *x, int64_t ldx, uint8_t *q, int64_t ldq, float *s, int64_t lds, int rows,
                                 int cols, int block_rows, cudaStream_t st) {
-  const unsigned across = block_rows == 1 ? (cols + 255) / 256 : (cols + 127) / 128;
-  const int64_t units = ((int64_t)rows + (block_rows == 1 ? 31 : 127)) / (block_rows == 1 ? 32 : 128) * across;
-  if (units > INT32_MAX) return cudaErrorInvalidValue;
+  const unsigned units = (unsigned)quant_units(rows, cols, block_rows);
   if (block_rows == 1)
-    return launch(quant_rows_kernel<T>, (unsigned)units, 256, 0, 1, st, x, ldx, q, ldq, s, lds, rows, cols, across);
-  return launch(quant_tiles_kernel<T>, (unsigned)units, 512, 0, 1, st, x, ldx, q, ldq, s, lds, rows, cols, across);
+    return launch(quant_rows_kernel<T>, units, 256, 0, 1, st, x, ldx, q, ldq, s, lds, rows, cols, (cols + 255) / 256);
+  return launch(quant_tiles_kernel<T>, units, 512, 0, 1, st, x, ldx, q, ldq, s, lds, rows, cols, (cols + 127) / 128);
 }
 
 }  // namespace fp8

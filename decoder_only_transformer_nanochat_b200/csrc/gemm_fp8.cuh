@@ -1002,7 +1002,6 @@ inline cudaError_t launch_rows(const GemmFp8Problem &g, const Plan &plan, int *s
   p.sa = g.sa; p.lsa = g.lsa; p.sb = g.sb; p.lsb = g.lsb;
   p.epi = g.epi; p.status = status;
   p.splits = plan.splits;
-  if (plan.tiles * p.splits > INT32_MAX) return cudaErrorInvalidValue;
   return fp8::launch(gemm_fp8_rows_kernel<TN, kMany>, (unsigned)(plan.tiles * p.splits), Cfg::kThreads, Cfg::kSmem, p.splits, st, mw,
                      mx, p);
 }
@@ -1026,9 +1025,8 @@ inline cudaError_t launch_pair(const GemmFp8Problem &g, const Plan &plan, int nu
     ok = ok && make_map(&md, g.D, g.M, cols, g.ldd, 64, 32);
   }
   if (!ok) return cudaErrorInvalidValue;
-  if (plan.tiles > INT32_MAX / 2) return cudaErrorInvalidValue;  // unit + grid stays an int
   p.kblocks = (g.K + BK - 1) / BK;
-  p.units = (int)plan.tiles;
+  p.units = (int)plan.tiles;  // at most 2^30: a unit and the grid together stay an int
   p.splits = plan.splits;
   p.sa = g.sa; p.lsa = g.lsa; p.sb = g.sb; p.lsb = g.lsb;
   p.status = status;

@@ -1404,9 +1404,8 @@ int nc_quant_fp8(const void *x, int64_t ldx, void *q, int64_t ldq, float *s, int
                  int block_rows, int dtype, void *stream) {
   if (!x || !q || !s) return NC_EINVAL;
   if (block_rows != 1 && block_rows != 128) return NC_EINVAL;
-  const int kbs = (cols + 127) / 128;
   if (rows < 1 || cols < 16 || cols % 16 || cols > (1 << 30) || ldx < cols || ldq < cols ||
-      lds < (block_rows == 1 ? rows : kbs))
+      lds < (block_rows == 1 ? rows : (cols + 127) / 128) || fp8::quant_units(rows, cols, block_rows) > INT32_MAX)
     return NC_ESHAPE;
   if (dtype != NC_F32 && dtype != NC_BF16) return NC_EUNSUPPORTED;
   if ((((uintptr_t)x | (uintptr_t)q) & 15) || ((uintptr_t)s & 3) || ldx % (dtype == NC_BF16 ? 8 : 4) || ldq % 16)
@@ -1430,6 +1429,7 @@ int nc_gemm_fp8(const void *A, int64_t lda, const float *sa, int64_t lsa, const 
   if (f8 && !sd) return NC_EINVAL;
   const int most = 1 << 30;
   if (M < 1 || N < 1 || K < 1 || M > most || N > most || K > most) return NC_ESHAPE;
+  if ((int64_t)((M + 127) / 128) * ((N + 127) / 128) > most) return NC_ESHAPE;  // every kernel's tiles then count in an int
   if (lda < K || ldb < K || ldd < N || lsa < M || lsb < (K + 127) / 128 || (f8 && lsd < M)) return NC_ESHAPE;
   const int64_t far = (int64_t)1 << 38;  // row strides the tensor maps hold (2^40 bytes)
   if (lda >= far || ldb >= far || ldd >= far) return NC_ESHAPE;

@@ -211,6 +211,7 @@ int nc_rope_qknorm_bwd(const nc_model *m, void *dqkv, const void *qkv, int64_t l
  * Their launches overlap the end of the kernel before them in the stream
  * (programmatic stream serialization); they touch memory only once that kernel
  * has completed, so the order of the stream's effects is what it always is.
+ * dtype is NC_BF16 or NC_F32 (else NC_EUNSUPPORTED).
  *
  * The residual's addition, RMSNorm and the 8-bit operand of the projection
  * that follows, in one pass:
@@ -220,7 +221,9 @@ int nc_rope_qknorm_bwd(const nc_model *m, void *dqkv, const void *qkv, int64_t l
  * x, res, x_out: [M, C] rows in dtype, x_out may equal x or res; q: [M, C]
  * e4m3; r: [M] fp32 or NULL.  The codes come from x_out (the norm scales a
  * row as a whole), s = r max|x_out| / 448.  A row that holds a NaN or an
- * infinity gets scales that are NaN in the blocks holding it at least.
+ * infinity gets scales that are NaN in the blocks holding it at least.  The
+ * squares are summed in fp32: finite values whose squares' sum reaches 2^128
+ * get r = 0 and scales of 0, as nc_rmsnorm's rows do.
  * 16 <= C <= 4096 with C % 16 == 0, lds >= M (else NC_ESHAPE); x, res, x_out,
  * q 16-byte aligned, s and r 4-byte aligned (else NC_EALIGN). */
 int nc_add_rmsnorm_fp8(const void *x, const void *res, void *x_out, void *q, float *s, int64_t lds, float *r,
@@ -229,8 +232,10 @@ int nc_add_rmsnorm_fp8(const void *x, const void *res, void *x_out, void *q, flo
 /* A matrix x [rows, cols] (dtype, row stride ldx elements) in 8 bits: q e4m3
  * with row stride ldq, s as above for block_rows 1 (activations: attention
  * outputs before their projection) or 128 (weights).  cols >= 16 with
- * cols % 16 == 0 (else NC_ESHAPE); x and q 16-byte aligned with 16-byte row
- * strides (else NC_EALIGN); other block_rows: NC_EINVAL. */
+ * cols % 16 == 0, cols <= 2^30, ldx, ldq >= cols, and no more than 2^31 - 1
+ * pieces of 32 rows x 256 columns (block_rows 1) or blocks of 128 x 128, else
+ * NC_ESHAPE; x and q 16-byte aligned with 16-byte row strides, s 4-byte aligned,
+ * else NC_EALIGN; other block_rows: NC_EINVAL. */
 int nc_quant_fp8(const void *x, int64_t ldx, void *q, int64_t ldq, float *s, int64_t lds, int rows, int cols,
                  int block_rows, int dtype, void *stream);
 
@@ -244,8 +249,8 @@ int nc_quant_fp8(const void *x, int64_t ldx, void *q, int64_t ldq, float *s, int
  *   D[m*ldd + n] = epilogue(acc)
  * A: activations [M, K] with 1 x 128 scales, B: weights [N, K] with 128 x 128
  * scales (y = x W^T).  Each block of K is summed on the tensor cores and the
- * scaled blocks in fp32, in an order that depends on the shape alone: the
- * same call gives the same bits.
+ * scaled blocks in fp32, in an order that depends on M, N, K and the device's
+ * number of SMs alone: the same call gives the same bits.
  * The product of a block's two scales is formed first, in fp32: all bits of the
  * result are there while it is 0 or at least 2^-126, it has steps of 2^-149
  * below that, and from 2^128 on the block's sums come out infinite or NaN.
@@ -255,8 +260,9 @@ int nc_quant_fp8(const void *x, int64_t ldx, void *q, int64_t ldq, float *s, int
  * NC_EINVAL.
  * The softcap is right to 2^-15 of its value, down to the smallest, before the
  * rounding to bf16.
- * 1 <= M, N, K <= 2^30, lda, ldb >= K, ldd >= N (each below 2^38), lsa (and
- * lsd) >= M, lsb >= ceil(K / 128), else NC_ESHAPE; A, B, D 16-byte aligned with 16-byte
+ * 1 <= M, N, K <= 2^30, no more than 2^30 blocks of 128 x 128 in D, lda, ldb >=
+ * K, ldd >= N (each below 2^38), lsa (and lsd) >= M, lsb >= ceil(K / 128), else
+ * NC_ESHAPE; A, B, D 16-byte aligned with 16-byte
  * row strides, the scales 4-byte aligned, else NC_EALIGN.  D and sd must not
  * overlap the operands.  A wait that ran out of time is reported through
  * nc_ops_status. */
