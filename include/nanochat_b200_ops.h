@@ -212,6 +212,7 @@ int nc_rope_qknorm_bwd(const nc_model *m, void *dqkv, const void *qkv, int64_t l
  * (programmatic stream serialization); they touch memory only once that kernel
  * has completed, so the order of the stream's effects is what it always is.
  * dtype is NC_BF16 or NC_F32 (else NC_EUNSUPPORTED).
+ * Outputs must not overlap inputs or one another, but where a call says so.
  *
  * The residual's addition, RMSNorm and the 8-bit operand of the projection
  * that follows, in one pass:
