@@ -132,37 +132,35 @@ template <> __device__ __forceinline__ uint2 quant8<float>(const float (&v)[8], 
 
 // The codes of fp32 values that stand in f32x2 pairs, as an epilogue has them,
 // by the same rule, RN_e4m3(RN(RN(448 v) / a)), without a division or a branch
-// per value: n = RN(448 v), y = RN(n / a) up to 1.5 units, and one step with
-// the residual, RN(y + (n - y a) / a), from the rounded reciprocal of a
-// (Markstein, "Computation of elementary functions on the IBM RISC System/6000
-// processor").  Where y is within a unit, which holds for n >= a in
-// significands, that is the quotient rounded to nearest; elsewhere it is off
-// by less than 2^-47 before its rounding, and n / a, as a quotient of 24-bit
-// numbers beside a border of 5 bits, stays that far from the middle between two
-// floats unless a's 24-bit significand is within 5 of a multiple of 2^20.  All
-// of those (and 40 to each side) give the right code for every border and
-// every n around it.  v and a are scaled by one power of two, exactly, so that
-// a is in [1, 4) (or, for a < 2^-119, at least 2^-30): nothing overflows, and no
-// residual of a value that gets a code but 0 is subnormal.  Against one product
-// with an approximate 448 / a this costs 15 us of 230 at 32,768 x 5120 x 1280
-// (two codes of bracketing products compared, the residual step only where they differ: 12 us).
+// per value: n = RN(448 v) times 1 / a held as two floats, rh + rl, each rounded
+// to nearest, as RN(n rh + RN(n rl)) (Brisebarre and Muller, "Correctly rounded
+// multiplication by arbitrary precision constants").  That is off by less than
+// 2^-47 before its rounding, for a in [1, 2) and n / a around 1; and n / a, as a
+// quotient of 24-bit numbers beside a border of 5 bits, stays that far from the
+// middle between two floats unless a's 24-bit significand is within 4 of a
+// multiple of 2^20.  All of those (and 40 to each side) give the right code for
+// every border and every n around it.  v and a are scaled by one power of two,
+// exactly, so that a is in [1, 4) (or, for a < 2^-119, at least 2^-30): nothing
+// overflows, and nothing that a code but 0 comes from is subnormal.  Against one
+// product with an approximate 448 / a this costs 8 us of 228 at 32,768 x 5120 x
+// 1280 (a residual step, y + (n - y a) / a, 14; two bracketing products and
+// that step only where their codes differ, 12).
 struct Ratio {
-  uint64_t k, ra, na;  // 448 and a scaled: n = k v; 1 / a; -a
+  uint64_t k, rh, rl;  // 448 scaled; 1 / a scaled
   __device__ __forceinline__ explicit Ratio(float a) {
     const int e = min(max((int)(__float_as_uint(a) >> 23), 8), 253);  // exponent field
     const float s = __uint_as_float((uint32_t)(254 - e) << 23), kf = kMax * s;
     const bool any = a > 0.f && a < INFINITY;  // else codes are 0, but for what is not finite
-    const float af = any ? a * s : 1.f, r = any ? __frcp_rn(af) : 0.f;
+    const float af = any ? a * s : 1.f, h = __frcp_rn(af), l = __fdiv_rn(fmaf(-h, af, 1.f), af);  // 1 - h a is exact
     k = f2(kf, kf);
-    ra = f2(r, r);
-    na = f2(-af, -af);
+    rh = any ? f2(h, h) : 0;
+    rl = any ? f2(l, l) : 0;
   }
   __device__ __forceinline__ uint32_t codes4(uint64_t v0, uint64_t v1) const {
     const uint64_t n0 = mul2(v0, k), n1 = mul2(v1, k);
-    const uint64_t y0 = mul2(n0, ra), y1 = mul2(n1, ra);
     float a, b, c, d;
-    f2split(fma2(fma2(y0, na, n0), ra, y0), a, b);
-    f2split(fma2(fma2(y1, na, n1), ra, y1), c, d);
+    f2split(fma2(n0, rh, mul2(n0, rl)), a, b);
+    f2split(fma2(n1, rh, mul2(n1, rl)), c, d);
     return cvt4(a, b, c, d);
   }
 };

@@ -730,7 +730,9 @@ __global__ void __launch_bounds__(PTHREADS, 1)
     // of the AHEAD before are used (a wait for the older of outstanding loads
     // would be one for the newer too).  Rows and columns outside the matrix
     // take the scales of the last one inside; they are not stored.
-    constexpr int AHEAD = 5;  // us at 16384 x 2048 x 8192: 2 262, 3 252, 4 248, 5 246, 6 262 (registers spill)
+    // us at 16384 x 2048 x 8192: 2 262, 3 252, 4 248, 5 246, 6 262.  At 5 the kernel
+    // spills four to seven registers, outside the loop over the K blocks' columns.
+    constexpr int AHEAD = 5;
     float fa[AHEAD], fb[AHEAD];
     const float *pa = nullptr, *pb = nullptr;
     auto fetch = [&](int kb) {
