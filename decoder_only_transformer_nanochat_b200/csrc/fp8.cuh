@@ -182,7 +182,7 @@ __device__ __forceinline__ float max16(float a) {
 // x' = x + res (rounded to T);  r = 1/sqrt(mean(x'^2) + eps);  y = r x' held in
 // e4m3 by blocks: since y / max|y| = x' / max|x'|, the codes come from x'
 // alone and only the scale, r max|x'| / 448, carries the norm.
-// Bandwidth-bound: 32,768 x 1280 bf16 rows 47 us, 6.3 TB/s; one row 2.7 us.
+// Bandwidth-bound: 32,768 x 1280 bf16 rows 46 us, 6.4 TB/s; one row 1.9 us.
 // WPR warps per row (one where there are rows enough to fill the SMs, four
 // otherwise): the row is read once and stays in registers, in its storage type
 // until it is used, so that all of its loads are in flight.
@@ -291,8 +291,9 @@ __global__ void __launch_bounds__(256) add_rmsnorm_fp8_kernel(const T *x, const 
 // 1 x 128 blocks: a warp takes 256 columns of four rows, 16 lanes to a block,
 // a CTA 32 rows of the same columns.  Lanes 0..3 and 16..19 then hold one
 // row's maximum each, so the four rows' scales take one division and one store.
-// 16,384 x 2048 bf16: 24 us, 4.2 TB/s: a CTA's loads, its arithmetic and its
-// stores follow one another, and no more CTAs fit an SM's registers.
+// 16,384 x 2048 bf16: 24 us, 4.2 TB/s: instruction issue (72 % of the slots, the
+// integer pipe 55 %, at 65,536 x 1280), in CTAs whose loads, arithmetic and
+// stores follow one another, five to an SM by their registers.
 // (Measured against CTAs that walk several units with the next one's loads in
 // flight: 23.9 against 26.8 us at 16,384 x 2048 bf16.)
 template <typename T>

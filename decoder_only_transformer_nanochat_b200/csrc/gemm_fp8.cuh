@@ -132,7 +132,7 @@ __device__ __forceinline__ float softcap8(float z) {
 // for them in its shared memory; after one cluster barrier it adds them in
 // rank order (the bits do not depend on which CTA ends first) and stores.
 //
-// Measured: one row x 1536 x 1280 4.8 us in a graph (launch, set-up, one load and
+// Measured: one row x 1536 x 1280 3.4 us in a graph (launch, set-up, one load and
 // one cluster barrier; the weights alone would take 0.3); 16 rows x 65,536 x
 // 1280 17.7 us in a row of calls, 4.9 TB/s.  The sums are 4-byte stores to the owner because a
 // pull needs a second cluster barrier (one row 6.5 us, pushed 5.4).
@@ -481,13 +481,14 @@ __global__ void __launch_bounds__(RowsCfg<TN, kMany>::kThreads, RowsCfg<TN, kMan
 // A thread's 128 columns are also one 1 x 128 output block, so the 8-bit
 // epilogue finds its maximum without leaving the thread.
 //
-// What bounds it: an accumulator's way round.  A K block takes about 780 cycles
-// where its MMAs take 512 (16384 x 2048 x 8192 with the residual add: 246 us,
-// 2.23 PFLOP/s; 32768 x 5120 x 1280 with relu^2 to 8 bits: 217 us, 1.98); the
-// loop without sums, one hand-over a tile, runs at 180 us and 3.06 PFLOP/s.
-// Two accumulators are all that TMEM holds at this tile, and a smaller tile
-// moves more operand bytes per product.  Handing over whole accumulators
-// measured 274 us, sixteen epilogue warps of 64 columns 7 % more than eight.
+// What bounds it: an accumulator's way round.  A K block takes about 900 cycles
+// where its MMAs take 512 (short runs: 16384 x 2048 x 8192 with the residual add
+// 248 us, 2.22 PFLOP/s; 32768 x 5120 x 1280 with relu^2 to 8 bits 228 us, 1.88;
+// long ones, under the power cap, 289 and 267 us); the loop without sums, one
+// hand-over a tile, runs at 180 us and 3.06 PFLOP/s.  Two accumulators are all
+// that TMEM holds at this tile; smaller tiles were not measured.  Handing over
+// whole accumulators measured 274 us, sixteen epilogue warps of 64 columns 7 %
+// more than eight.
 //
 // Few tiles leave SMs idle, so K is cut over the pairs of a larger cluster (2
 // or 4): each CTA then leaves its sums in its ring's memory and adds, for its
