@@ -13,7 +13,8 @@
 // within 2^-20 of z, so rounding it to 16 significant bits first puts every border case back
 // on the border and moves no other value across one: the result is the
 // round-to-nearest-even of the exact quotient, without a division per value.
-// fp32 inputs take RN(RN(448 v) / a), one IEEE division per value.
+// fp32 inputs take RN(RN(448 v) / a): the same approximate product decides, but
+// for the one value in 2^14 so close to a border that the division has to.
 #pragma once
 
 #include "elementwise.cuh"
